@@ -16,6 +16,7 @@ from ._lib import (QLoraError, lib, qlora_double_quant, qlora_double_quant_works
                    qlora_linear_fwd_wait_counter_offset, qlora_linear_fwd_workspace, qlora_merge,
                    qlora_nf4_dequant, qlora_nf4_levels,
                    qlora_nf4_quantize, qlora_nf4_quantize_bf16, qlora_nf4_sizes)
+from .kv import KVCache, kv_attention, kv_attention_workspace, kv_cache, kv_read, kv_write  # noqa: F401
 
 
 @dataclasses.dataclass

@@ -44,6 +44,15 @@ SIGNATURES = {
                                         _p, _p, _p, _p, _p, _sz, _p]),
 }
 
+# the same for include/qlora_kv.h
+KV_SIGNATURES = {
+    "qlora_kv_write": (ctypes.c_int, [_p, _p, _p, _int, _i64, _p, _p, _p]),
+    "qlora_kv_read": (ctypes.c_int, [_p, _p, _i64, _int, _p, _p, _p]),
+    "qlora_kv_attention_workspace": (_sz, [_p, _i64, _i64, _i64, _i64, _i64, _i64]),
+    "qlora_kv_attention": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _f, _int,
+                                          _i64, _p, _p, _p, _sz, _p]),
+}
+
 
 class QLoraError(RuntimeError):
     def __init__(self, status: int, where: str):
@@ -62,7 +71,7 @@ def lib() -> ctypes.CDLL:
             raise ImportError(f"libqlora.so is not built ({LIB_PATH}); run "
                               "`python -m bit_nf4_quantized_quant_amd.build` (needs hipcc)")
         handle = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in SIGNATURES.items():
+        for name, (res, args) in {**SIGNATURES, **KV_SIGNATURES}.items():
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args

@@ -1,0 +1,81 @@
+// The 4-bit key/value cache as its kernels see it, and their launchers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "nf4_table.h"
+
+namespace qlora {
+namespace kv {
+
+// n / d for 0 <= n < 2^31 and a fixed 2 <= d < 2^31 by one 32-bit multiply:
+// with 2^b the smallest power of two >= d and m = ceil(2^(31+b) / d), which
+// fits 32 bits, m n / 2^(31+b) exceeds n / d by less than n / 2^(31+b) < 1 / d.
+struct FastDiv {
+  uint32_t d, m, shift;
+};
+
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t b = 1;
+  while ((uint64_t(1) << b) < d) ++b;
+  return FastDiv{d, (uint32_t)(((uint64_t(1) << (31 + b)) + d - 1) / d), b - 1};
+}
+
+__device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) { return __umulhi(n, f.m) >> f.shift; }
+
+// One cache (device pointers); row (page heads + head) page_size + offset of a
+// codes tensor is D / 2 bytes long, of a scales tensor D / 64 bf16 numbers.
+struct Cache {
+  uint8_t* codes[2];     // keys, values
+  uint16_t* scales[2];
+  uint32_t pages, heads, page_size, rows;   // rows = pages * page_size (token slots)
+  FastDiv page_div;
+  int D;
+  int table;
+};
+
+struct WriteArgs {
+  Cache c;
+  const void* x[2];          // k, v
+  int64_t token_stride[2], head_stride[2];
+  const int32_t* slots;
+  int64_t tokens;
+  bool f32;
+};
+
+struct ReadArgs {
+  Cache c;
+  const int32_t* slots;
+  int64_t tokens;
+  void* out[2];
+  bool f32;
+};
+
+struct AttnArgs {
+  Cache c;
+  const uint16_t* q;
+  int64_t token_stride, head_stride;
+  int64_t tokens;
+  int64_t q_heads;
+  const int32_t* block_table;
+  int64_t table_width;
+  const int32_t* lengths;
+  const int32_t* q_starts;   // or null
+  int64_t seqs, max_q, max_len;
+  float scale;
+  int causal;
+  int64_t window;
+  uint16_t* out;
+  float* lse;                // or null
+  void* workspace;
+};
+
+hipError_t launch_kv_write(const WriteArgs& a, hipStream_t s);
+hipError_t launch_kv_read(const ReadArgs& a, hipStream_t s);
+size_t kv_attention_workspace_bytes(const AttnArgs& a);
+hipError_t launch_kv_attention(const AttnArgs& a, hipStream_t s);
+
+}  // namespace kv
+}  // namespace qlora

@@ -1,0 +1,189 @@
+// C ABI of the 4-bit key/value cache: argument validation on the host, then
+// kernel launches on the caller's stream.  Every check runs before the first
+// HIP call.
+#include <algorithm>
+
+#include "kv.h"
+#include "launch.h"
+#include "qlora_kv.h"
+
+using namespace qlora;
+
+namespace {
+
+constexpr int64_t kMaxRows = int64_t(1) << 31;    // pages * heads * page_size: 32-bit row numbers
+constexpr int64_t kMaxCount = int64_t(1) << 31;   // tokens, lengths: 32-bit positions
+constexpr int64_t kMaxGrid = int64_t(1) << 31;    // workgroups along a grid's x axis
+constexpr int64_t kMaxSeqs = 65535;               // a grid's z axis
+constexpr int64_t kMaxHeads = 65535;              // a grid's y axis
+constexpr int64_t kMaxStride = int64_t(1) << 40;  // element strides
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int status_of(hipError_t e) { return e == hipSuccess ? QLORA_OK : QLORA_EHIP; }
+
+// The cache's sizes; its pointers are checked where they are used.
+int check_sizes(const qlora_kv_cache* c) {
+  if (!c || c->pages < 0 || c->kv_heads < 0 || c->page_size < 0 || c->head_dim < 0) return QLORA_EINVAL;
+  if (c->table < 0 || c->table >= kCodeTables) return QLORA_EINVAL;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return QLORA_ESHAPE;
+  if (c->page_size == 0 || c->page_size % 16 != 0) return QLORA_ESHAPE;
+  if (c->pages < 1 || c->kv_heads < 1 || c->kv_heads > kMaxHeads) return QLORA_ESHAPE;
+  if (c->page_size >= kMaxRows || c->pages >= kMaxRows || c->page_size * c->kv_heads >= kMaxRows ||
+      c->page_size * c->kv_heads * c->pages >= kMaxRows)
+    return QLORA_ESHAPE;
+  return QLORA_OK;
+}
+
+int check_pointers(const qlora_kv_cache* c) {
+  if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return QLORA_EINVAL;
+  if (!aligned(c->k_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_codes, 16) || !aligned(c->v_scales, 16))
+    return QLORA_EINVAL;
+  return QLORA_OK;
+}
+
+kv::Cache device_cache(const qlora_kv_cache* c) {
+  kv::Cache d;
+  d.codes[0] = c->k_codes;
+  d.codes[1] = c->v_codes;
+  d.scales[0] = c->k_scales;
+  d.scales[1] = c->v_scales;
+  d.pages = (uint32_t)c->pages;
+  d.heads = (uint32_t)c->kv_heads;
+  d.page_size = (uint32_t)c->page_size;
+  d.rows = (uint32_t)(c->pages * c->page_size);
+  d.page_div = kv::fast_div((uint32_t)c->page_size);
+  d.D = (int)c->head_dim;
+  d.table = c->table;
+  return d;
+}
+
+// Workgroups of the read and write kernels: 32 runs of 64 elements each.
+int check_tokens(const qlora_kv_cache* c, int64_t tokens, int dtype) {
+  if (tokens < 0 || (dtype != QLORA_KV_BF16 && dtype != QLORA_KV_F32)) return QLORA_EINVAL;
+  if (tokens >= kMaxCount) return QLORA_ESHAPE;
+  const int64_t per = 32 / (c->head_dim / 64);
+  if ((tokens + per - 1) / per * c->kv_heads >= kMaxGrid) return QLORA_ESHAPE;
+  return QLORA_OK;
+}
+
+int check_stride(int64_t stride, int64_t piece) {
+  if (stride < 0) return QLORA_EINVAL;
+  return stride % piece || stride >= kMaxStride ? QLORA_ESHAPE : QLORA_OK;
+}
+
+int check_attention(const qlora_kv_cache* c, int64_t q_heads, int64_t tokens, int64_t seqs, int64_t max_q,
+                    int64_t max_len, int64_t window) {
+  const int st = check_sizes(c);
+  if (st) return st;
+  if (q_heads < 0 || tokens < 0 || seqs < 0 || max_q < 0 || max_len < 0 || window < 0) return QLORA_EINVAL;
+  if (q_heads < 1 || q_heads % c->kv_heads || q_heads > kMaxHeads) return QLORA_ESHAPE;
+  if (tokens >= kMaxCount || max_len >= kMaxCount || max_q >= kMaxCount / q_heads || seqs > kMaxSeqs) return QLORA_ESHAPE;
+  return QLORA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qlora_kv_write(const qlora_kv_cache* cache, const void* k, const void* v, int dtype, int64_t tokens,
+                   const int64_t strides[4], const int32_t* slots, void* stream) {
+  int st = check_sizes(cache);
+  if (!st) st = check_tokens(cache, tokens, dtype);
+  if (st || tokens == 0) return st;
+  if ((st = check_pointers(cache))) return st;
+  if (!k || !v || !strides || !slots) return QLORA_EINVAL;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4)) return QLORA_EINVAL;
+  for (int i = 0; i < 4; ++i)
+    if ((st = check_stride(strides[i], dtype == QLORA_KV_F32 ? 4 : 8))) return st;
+  kv::WriteArgs a;
+  a.c = device_cache(cache);
+  a.x[0] = k;
+  a.x[1] = v;
+  a.token_stride[0] = strides[0];
+  a.head_stride[0] = strides[1];
+  a.token_stride[1] = strides[2];
+  a.head_stride[1] = strides[3];
+  a.slots = slots;
+  a.tokens = tokens;
+  a.f32 = dtype == QLORA_KV_F32;
+  return status_of(kv::launch_kv_write(a, (hipStream_t)stream));
+}
+
+int qlora_kv_read(const qlora_kv_cache* cache, const int32_t* slots, int64_t tokens, int dtype, void* k, void* v,
+                  void* stream) {
+  int st = check_sizes(cache);
+  if (!st) st = check_tokens(cache, tokens, dtype);
+  if (st || tokens == 0) return st;
+  if ((st = check_pointers(cache))) return st;
+  if (!k || !v || !slots) return QLORA_EINVAL;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4)) return QLORA_EINVAL;
+  kv::ReadArgs a;
+  a.c = device_cache(cache);
+  a.slots = slots;
+  a.tokens = tokens;
+  a.out[0] = k;
+  a.out[1] = v;
+  a.f32 = dtype == QLORA_KV_F32;
+  return status_of(kv::launch_kv_read(a, (hipStream_t)stream));
+}
+
+size_t qlora_kv_attention_workspace(const qlora_kv_cache* cache, int64_t q_heads, int64_t tokens, int64_t seqs,
+                                    int64_t max_q, int64_t max_len, int64_t window) {
+  if (check_attention(cache, q_heads, tokens, seqs, max_q, max_len, window)) return 0;
+  kv::AttnArgs a{};
+  a.c = device_cache(cache);
+  a.q_heads = q_heads;
+  a.tokens = tokens;
+  a.seqs = seqs;
+  a.max_q = max_q;
+  a.max_len = max_len;
+  a.window = window;
+  return kv::kv_attention_workspace_bytes(a);
+}
+
+int qlora_kv_attention(const qlora_kv_cache* cache, const uint16_t* q, const int64_t q_strides[2], int64_t tokens,
+                       int64_t q_heads, const int32_t* block_table, int64_t table_width, const int32_t* lengths,
+                       const int32_t* q_starts, int64_t seqs, int64_t max_q, int64_t max_len, float scale, int causal,
+                       int64_t window, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  int st = check_attention(cache, q_heads, tokens, seqs, max_q, max_len, window);
+  if (st) return st;
+  if (table_width < 0) return QLORA_EINVAL;
+  // without q_starts every sequence has max_q queries
+  if (!q_starts && (max_q == 0 ? tokens != 0 : tokens / max_q != seqs || tokens % max_q)) return QLORA_ESHAPE;
+  if (tokens == 0 || seqs == 0 || max_q == 0) return QLORA_OK;
+  if (table_width >= kMaxCount / cache->page_size || seqs * table_width >= kMaxCount) return QLORA_ESHAPE;
+  if ((st = check_pointers(cache))) return st;
+  if (!q || !q_strides || !lengths || !out || (table_width > 0 && !block_table)) return QLORA_EINVAL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lengths, 4) || !aligned(block_table, 4) ||
+      !aligned(q_starts, 4) || !aligned(lse, 4))
+    return QLORA_EINVAL;
+  for (int i = 0; i < 2; ++i)
+    if ((st = check_stride(q_strides[i], 8))) return st;
+  kv::AttnArgs a{};
+  a.c = device_cache(cache);
+  a.q = q;
+  a.token_stride = q_strides[0];
+  a.head_stride = q_strides[1];
+  a.tokens = tokens;
+  a.q_heads = q_heads;
+  a.block_table = block_table;
+  a.table_width = table_width;
+  a.lengths = lengths;
+  a.q_starts = q_starts;
+  a.seqs = seqs;
+  a.max_q = max_q;
+  a.max_len = max_len;
+  a.scale = scale;
+  a.causal = causal != 0;
+  a.window = window;
+  a.out = out;
+  a.lse = lse;
+  const size_t need = kv::kv_attention_workspace_bytes(a);
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return QLORA_EINVAL;
+  a.workspace = workspace;
+  return status_of(kv::launch_kv_attention(a, (hipStream_t)stream));
+}
+
+}  // extern "C"

@@ -190,4 +190,29 @@ const Nf4Buckets& code_buckets(int type) {
   return bk[type];
 }
 
+const KvBuckets& kv_buckets(int type) {
+  static KvBuckets bk[kCodeTables];
+  static std::once_flag once;
+  std::call_once(once, [] {
+    for (int ty = 0; ty < kCodeTables; ++ty) {
+      float thr[15];   // the smallest fp32 number above each midpoint
+      for (int j = 0; j < 15; ++j) {
+        const double mid = ((double)code_table(ty).level[j] + (double)code_table(ty).level[j + 1]) / 2;
+        thr[j] = (float)mid;
+        if ((double)thr[j] <= mid) thr[j] = std::nextafter(thr[j], INFINITY);
+      }
+      for (int q = 0; q < kKvBuckets; ++q) {
+        const double lo = (q - 16.5) / 16.0, hi = (q - 15.5) / 16.0;
+        bk[ty].thr[q] = INFINITY;
+        bk[ty].base[q] = 0;
+        for (const float v : thr) {
+          if (v < lo) ++bk[ty].base[q];
+          if (v >= lo && v < hi) bk[ty].thr[q] = v;
+        }
+      }
+    }
+  });
+  return bk[type];
+}
+
 }  // namespace qlora

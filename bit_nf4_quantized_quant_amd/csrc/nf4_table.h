@@ -37,6 +37,23 @@ struct Nf4Buckets {
 
 const Nf4Buckets& code_buckets(int type);
 
+// The cache's code search: the code of a quotient x is the number of midpoints
+// between neighbouring levels that lie below it (FP4's two zeros count as
+// neighbours with a midpoint at 0, so a small positive x gets the upper one).
+// Bucket q (0..33) is [(q - 16.5)/16, (q - 15.5)/16), its index the integer
+// part of 16 x + 16.5; thr[q] is the smallest fp32 number above the bucket's
+// one midpoint (+inf if none), base[q] the midpoints below the bucket.  Every
+// table's midpoints, the one at zero included, lie at least 2^-10 away from
+// these edges and no two share a bucket, so the search holds for every table
+// and for quotients up to 1 + 2^-5 in magnitude.
+constexpr int kKvBuckets = 34;
+struct KvBuckets {
+  float thr[kKvBuckets];
+  unsigned int base[kKvBuckets];
+};
+
+const KvBuckets& kv_buckets(int type);
+
 // The levels as the decode kernels feed them to bf16 dot products and matrix
 // cores: bf16(kappa * L[i]), with the block sums scaled by 1/kappa at the end.
 // kappa is the smallest integer in 1..64 for which every kappa * L[i] is a

@@ -1,0 +1,182 @@
+"""The 4-bit key/value cache: allocation, storing, reading back, attention.
+
+Bindings of include/qlora_kv.h.  As in ``_lib``, nothing here computes: the
+helpers check types and shapes, allocate outputs and workspaces with torch and
+pass device pointers to libqlora.so.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import dataclasses
+
+from ._lib import _check, _i64, _stream, lib
+
+
+class _CacheStruct(ctypes.Structure):
+    """struct qlora_kv_cache"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales")] + \
+               [(n, _i64) for n in ("pages", "kv_heads", "page_size", "head_dim")] + [("table", ctypes.c_int32)]
+
+
+@dataclasses.dataclass(frozen=True, eq=False)
+class KVCache:
+    """Keys and values of tokens in 4-bit codes, in pages (device tensors).
+
+    k_codes, v_codes: uint8 [pages, kv_heads, page_size, head_dim / 2];
+    k_scales, v_scales: bf16 [pages, kv_heads, page_size, head_dim / 64];
+    table: code table, 0 NF4, 1 uniform 4-bit, 2 FP4.  Token slot s is row
+    s % page_size of page s // page_size.
+    """
+    k_codes: "object"
+    k_scales: "object"
+    v_codes: "object"
+    v_scales: "object"
+    table: int = 0
+
+    def __post_init__(self):
+        import torch
+        pages, heads, page, half = self.k_codes.shape
+        for name, dtype, last in (("k_codes", torch.uint8, half), ("v_codes", torch.uint8, half),
+                                  ("k_scales", torch.bfloat16, half // 32), ("v_scales", torch.bfloat16, half // 32)):
+            t = getattr(self, name)
+            if (not t.is_cuda or t.device != self.k_codes.device or t.dtype != dtype
+                    or t.shape != (pages, heads, page, last) or not t.is_contiguous()):
+                raise ValueError(f"KVCache: {name} must be a contiguous {dtype} GPU tensor "
+                                 f"[{pages}, {heads}, {page}, {last}]")
+        s = _CacheStruct(self.k_codes.data_ptr(), self.k_scales.data_ptr(), self.v_codes.data_ptr(),
+                         self.v_scales.data_ptr(), pages, heads, page, 2 * half, self.table)
+        object.__setattr__(self, "_struct", s)
+        object.__setattr__(self, "_ref", ctypes.byref(s))
+
+    @property
+    def pages(self) -> int:
+        return self._struct.pages
+
+    @property
+    def kv_heads(self) -> int:
+        return self._struct.kv_heads
+
+    @property
+    def page_size(self) -> int:
+        return self._struct.page_size
+
+    @property
+    def head_dim(self) -> int:
+        return self._struct.head_dim
+
+
+def kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda", table: int = 0) -> KVCache:
+    """An empty cache: every row reads back as zero."""
+    import torch
+    if page_size < 1 or page_size % 16 or head_dim not in (64, 128, 256):
+        raise ValueError("kv_cache: page_size must be a multiple of 16 and head_dim 64, 128 or 256")
+    t = [torch.zeros((pages, kv_heads, page_size, n), dtype=d, device=device)
+         for n, d in ((head_dim // 2, torch.uint8), (head_dim // 64, torch.bfloat16)) * 2]
+    return KVCache(*t, table)
+
+
+def _dtype_code(dtype) -> int:
+    import torch
+    if dtype == torch.bfloat16:
+        return 0
+    if dtype == torch.float32:
+        return 1
+    raise ValueError(f"the key/value cache stores and returns bf16 or fp32, not {dtype}")
+
+
+def _ints(t, name, shape, device):
+    """A contiguous int32 tensor on the cache's device, as a pointer."""
+    import torch
+    if t.dtype != torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on the cache's device")
+    return t.data_ptr()
+
+
+def kv_write(k, v, cache: KVCache, slots, stream=None) -> None:
+    """Store the tokens k, v [tokens, kv_heads, head_dim] (bf16 or fp32; slices of
+    a fused projection are fine) at `slots` (int32 [tokens]); a token whose slot
+    is negative or past the cache is skipped."""
+    n = k.shape[0]
+    shape = (n, cache.kv_heads, cache.head_dim)
+    device = cache.k_codes.device
+    if k.shape != shape or v.shape != shape or k.dtype != v.dtype or k.device != device or v.device != device:
+        raise ValueError(f"kv_write: k and v must be {shape} tensors of one type on the cache's device")
+    ks, vs = k.stride(), v.stride()
+    if ks[2] != 1 or vs[2] != 1:
+        raise ValueError("kv_write: the last axis of k and v must be contiguous")
+    _check(lib().qlora_kv_write(cache._ref, k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype), n,
+                                (_i64 * 4)(ks[0], ks[1], vs[0], vs[1]), _ints(slots, "slots", (n,), device),
+                                _stream(stream)), "qlora_kv_write")
+
+
+def kv_read(cache: KVCache, slots, dtype=None, stream=None):
+    """The tokens at `slots` (int32 [n]) as (k, v), each [n, kv_heads, head_dim] in
+    `dtype` (bf16 unless given; or fp32); zeros for a skipped slot."""
+    import torch
+    if dtype is None:
+        dtype = torch.bfloat16
+    n, device = slots.shape[0], cache.k_codes.device
+    k = torch.empty((n, cache.kv_heads, cache.head_dim), dtype=dtype, device=device)
+    v = torch.empty_like(k)
+    _check(lib().qlora_kv_read(cache._ref, _ints(slots, "slots", (n,), device), n, _dtype_code(dtype), k.data_ptr(),
+                               v.data_ptr(), _stream(stream)), "qlora_kv_read")
+    if stream is not None:   # allocated on the current stream, written on another
+        k.record_stream(stream)
+        v.record_stream(stream)
+    return k, v
+
+
+def kv_attention_workspace(cache: KVCache, q_heads: int, tokens: int, seqs: int, max_q: int, max_len: int,
+                           window: int = 0):
+    """A workspace for kv_attention calls of at most these sizes (any content)."""
+    import torch
+    n = lib().qlora_kv_attention_workspace(cache._ref, q_heads, tokens, seqs, max_q, max_len, window)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=cache.k_codes.device)
+
+
+def kv_attention(q, cache: KVCache, block_table, lengths, q_starts=None, max_q=None, max_len=None, scale=None,
+                 causal: bool = True, window: int = 0, want_lse: bool = False, workspace=None, stream=None):
+    """Attention of new tokens over the cache; returns (out bf16 like q, lse fp32 [tokens, q_heads] or None).
+
+    q: bf16 [tokens, q_heads, head_dim], the queries of the sequences one after
+    the other.  block_table: int32 [seqs, width], the pages of each sequence.
+    lengths: int32 [seqs], cached tokens of each, its queries' own (its last
+    ones) among them.  q_starts: int32 [seqs + 1], where each sequence's queries
+    begin in q, or None where all have tokens / seqs of them.  max_q, max_len:
+    bounds on one sequence's queries (needed with q_starts) and length (the block
+    table's reach unless given); a tight max_len lets the launch fit the work.
+    scale: head_dim ** -0.5 unless given.  A query sees the positions up to its
+    own (causal) or all, and only the last `window` of them where window > 0; one
+    that sees none gets zeros and an lse of -infinity.
+    """
+    import torch
+    tokens, heads, dim = q.shape
+    seqs, width = block_table.shape
+    device = cache.k_codes.device
+    qs = q.stride()
+    if q.dtype != torch.bfloat16 or dim != cache.head_dim or q.device != device or qs[2] != 1:
+        raise ValueError(f"kv_attention: q must be bf16 [tokens, q_heads, {cache.head_dim}] on the cache's device, "
+                         "its last axis contiguous")
+    if max_q is None:
+        if q_starts is not None:
+            raise ValueError("kv_attention: q_starts needs max_q")
+        max_q = tokens // seqs if seqs else 0
+    if max_len is None:
+        max_len = width * cache.page_size
+    out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=device)
+    lse = torch.empty((tokens, heads), dtype=torch.float32, device=device) if want_lse else None
+    if workspace is None:
+        workspace = kv_attention_workspace(cache, heads, tokens, seqs, max_q, max_len, window)
+    _check(lib().qlora_kv_attention(
+        cache._ref, q.data_ptr(), (_i64 * 2)(qs[0], qs[1]), tokens, heads,
+        _ints(block_table, "block_table", (seqs, width), device), width, _ints(lengths, "lengths", (seqs,), device),
+        None if q_starts is None else _ints(q_starts, "q_starts", (seqs + 1,), device), seqs, max_q, max_len,
+        dim ** -0.5 if scale is None else scale, causal, window, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream)),
+        "qlora_kv_attention")
+    if stream is not None:   # allocated on the current stream, used on another
+        for t in (out, lse, workspace):
+            if t is not None:
+                t.record_stream(stream)
+    return out, lse

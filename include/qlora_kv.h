@@ -1,0 +1,128 @@
+/*
+ * qlora_kv.h -- C ABI of libqlora.so, second part: a paged key/value cache held
+ * in the 4-bit codes of qlora.h's tables, and attention over it, on one AMD
+ * MI355X (gfx950).
+ *
+ * The cache.  Tokens live in `pages` pages of `page_size` rows.  A page keeps,
+ * for each of `kv_heads` heads, page_size rows of head_dim codes (two codes per
+ * byte, the even element in the low nibble, as in the weights' codes) and one
+ * bf16 scale per run of 64 elements, for the keys and for the values:
+ *
+ *     codes  uint8  [pages, kv_heads, page_size, head_dim / 2]
+ *     scales bf16   [pages, kv_heads, page_size, head_dim / 64]
+ *
+ * Token `slot` is row slot % page_size of page slot / page_size.  An element
+ * stands for level[code] * scale, level being the table's fp32 level
+ * (qlora_nf4_levels).  There is no second quantization of the scales: a
+ * tensor mean, which the weights' double quantization is centred on, does not
+ * exist for tokens that arrive one at a time.
+ *
+ * The storing rule for a run x of 64 elements, a = max |x|:
+ *     scale = bf16(min(a, largest finite bf16)), round to nearest even;
+ *             0 where a < 2^-126, NaN where a is infinite or NaN;
+ *     code  = how many midpoints between neighbouring levels lie below
+ *             fl(x * fl(1 / scale)) in fp32: the nearest level, the lower one
+ *             on a tie (the quotient counts as 0 where scale is 0; FP4's two
+ *             zeros are neighbours with their midpoint at 0).
+ * So a run with a non-finite element reads back as NaN, and every other run is
+ * finite whatever it holds.
+ *
+ * Conventions are those of qlora.h: device pointers, caller-owned buffers, no
+ * allocation and no synchronization, every check before the first launch.  The
+ * token and head strides of k, v and q are element counts, so slices of one
+ * fused projection's output are passed as they are; the last axis is
+ * contiguous.  Empty problems (no tokens) return QLORA_OK and queue nothing.
+ */
+#ifndef QLORA_KV_H
+#define QLORA_KV_H
+
+#include "qlora.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define QLORA_KV_BF16 0
+#define QLORA_KV_F32 1
+
+typedef struct qlora_kv_cache {
+  uint8_t* k_codes;   /* 16-byte aligned */
+  uint16_t* k_scales; /* 16-byte aligned */
+  uint8_t* v_codes;   /* 16-byte aligned */
+  uint16_t* v_scales; /* 16-byte aligned */
+  int64_t pages;
+  int64_t kv_heads;
+  int64_t page_size;  /* a multiple of 16 */
+  int64_t head_dim;   /* 64, 128 or 256 */
+  int32_t table;      /* QLORA_TABLE_* */
+} qlora_kv_cache;
+/* pages * kv_heads * page_size must stay below 2^31 (rows of one tensor). */
+
+/*
+ * qlora_kv_write: store `tokens` tokens.  k, v: [tokens, kv_heads, head_dim],
+ * bf16 (QLORA_KV_BF16) or fp32 (QLORA_KV_F32) by `dtype`, 16-byte aligned with
+ * strides of whole 16-byte pieces; the strides are {token, head} of k, then of
+ * v.  slots: int32 [tokens]; a token whose slot is negative or past the cache
+ * is skipped (padding).  Two tokens of one call with the same slot leave either
+ * one's runs there.
+ */
+int qlora_kv_write(const qlora_kv_cache* cache, const void* k, const void* v, int dtype, int64_t tokens,
+                   const int64_t strides[4], const int32_t* slots, void* stream);
+
+/*
+ * qlora_kv_read: the values of `tokens` tokens, as bf16 (round to nearest
+ * even) or fp32 by `dtype`.  k, v: outputs [tokens, kv_heads, head_dim],
+ * contiguous, 16-byte aligned.  slots as in qlora_kv_write; a skipped token's
+ * outputs are zero.
+ */
+int qlora_kv_read(const qlora_kv_cache* cache, const int32_t* slots, int64_t tokens, int dtype, void* k, void* v,
+                  void* stream);
+
+/*
+ * Attention of new tokens over the cache.
+ *
+ * The queries of `seqs` sequences stand one sequence after the other in q
+ * [tokens, q_heads, head_dim] (bf16): those of sequence b are rows q_starts[b]
+ * .. q_starts[b + 1] - 1, or max_q each where q_starts is NULL.  lengths[b]
+ * counts the cached tokens of sequence b, its queries' own among them: the n_b
+ * queries are its last n_b tokens, query i at position lengths[b] - n_b + i.
+ * Page j of sequence b is block_table[b * table_width + j].  Query head h reads
+ * kv head h / (q_heads / kv_heads).
+ *
+ * A query at position p sees the positions j < lengths[b] with
+ *     j <= p           where causal is set, and
+ *     j > p - window   where window > 0;
+ * out = sum_j softmax_j(scale q.k_j) v_j (bf16), and lse (optional, fp32
+ * [tokens, q_heads]) = ln sum_j exp(scale q.k_j).  A query that sees nothing
+ * gets zeros, and -infinity.  What a query does not see does not enter its
+ * result, non-finite values included.  A position whose page number is not in
+ * [0, pages) is seen by nobody.
+ *
+ * max_q and max_len bound the queries and the length of one sequence; they size
+ * the launch.  Only a sequence's first max_q queries and only the positions
+ * that table_width pages hold are computed with; a length beyond max_len is
+ * still read whole, only slower.
+ *
+ * The scores and the sums are formed by fp16 matrix products of the levels
+ * (fp16 holds them to 2^-12, with the scales applied in powers of two) with
+ * fp32 accumulation; the softmax statistics are fp32.
+ *
+ * q: 16-byte aligned, strides {token, head} of whole 16-byte pieces.  out:
+ * contiguous [tokens, q_heads, head_dim], 16-byte aligned.  workspace: at least
+ * qlora_kv_attention_workspace bytes of any content, 256-byte aligned; not
+ * shared by calls that may run at the same time.
+ */
+size_t qlora_kv_attention_workspace(const qlora_kv_cache* cache, int64_t q_heads, int64_t tokens, int64_t seqs,
+                                    int64_t max_q, int64_t max_len, int64_t window);
+
+int qlora_kv_attention(const qlora_kv_cache* cache, const uint16_t* q, const int64_t q_strides[2], int64_t tokens,
+                       int64_t q_heads, const int32_t* block_table, int64_t table_width, const int32_t* lengths,
+                       const int32_t* q_starts, int64_t seqs, int64_t max_q, int64_t max_len, float scale, int causal,
+                       int64_t window, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* QLORA_KV_H */
