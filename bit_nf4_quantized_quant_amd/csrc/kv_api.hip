@@ -13,9 +13,9 @@ namespace {
 
 constexpr int64_t kMaxRows = int64_t(1) << 31;    // pages * heads * page_size: 32-bit row numbers
 constexpr int64_t kMaxCount = int64_t(1) << 31;   // tokens, lengths: 32-bit positions
-constexpr int64_t kMaxGrid = int64_t(1) << 31;    // workgroups along a grid's x axis
-constexpr int64_t kMaxSeqs = 65535;               // a grid's z axis
-constexpr int64_t kMaxHeads = 65535;              // a grid's y axis
+constexpr int64_t kMaxGrid = int64_t(1) << 24;    // workgroups of 256 threads of one launch: 2^32 threads
+constexpr int64_t kMaxSeqs = 65535;               // a grid's y axis
+constexpr int64_t kMaxHeads = 8192;
 constexpr int64_t kMaxStride = int64_t(1) << 40;  // element strides
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -63,7 +63,7 @@ int check_tokens(const qlora_kv_cache* c, int64_t tokens, int dtype) {
   if (tokens < 0 || (dtype != QLORA_KV_BF16 && dtype != QLORA_KV_F32)) return QLORA_EINVAL;
   if (tokens >= kMaxCount) return QLORA_ESHAPE;
   const int64_t per = 32 / (c->head_dim / 64);
-  if ((tokens + per - 1) / per * c->kv_heads >= kMaxGrid) return QLORA_ESHAPE;
+  if ((tokens + per - 1) / per * c->kv_heads >= kMaxGrid / 2) return QLORA_ESHAPE;
   return QLORA_OK;
 }
 
@@ -131,6 +131,7 @@ int qlora_kv_read(const qlora_kv_cache* cache, const int32_t* slots, int64_t tok
 size_t qlora_kv_attention_workspace(const qlora_kv_cache* cache, int64_t q_heads, int64_t tokens, int64_t seqs,
                                     int64_t max_q, int64_t max_len, int64_t window) {
   if (check_attention(cache, q_heads, tokens, seqs, max_q, max_len, window)) return 0;
+  if (tokens == 0 || seqs == 0 || max_q == 0) return 0;
   kv::AttnArgs a{};
   a.c = device_cache(cache);
   a.q_heads = q_heads;
@@ -153,7 +154,7 @@ int qlora_kv_attention(const qlora_kv_cache* cache, const uint16_t* q, const int
   // without q_starts every sequence has max_q queries
   if (!q_starts && (max_q == 0 ? tokens != 0 : tokens / max_q != seqs || tokens % max_q)) return QLORA_ESHAPE;
   if (tokens == 0 || seqs == 0 || max_q == 0) return QLORA_OK;
-  if (table_width >= kMaxCount / cache->page_size || seqs * table_width >= kMaxCount) return QLORA_ESHAPE;
+  if (table_width >= kMaxCount / 2 / cache->page_size || seqs * table_width >= kMaxCount) return QLORA_ESHAPE;
   if ((st = check_pointers(cache))) return st;
   if (!q || !q_strides || !lengths || !out || (table_width > 0 && !block_table)) return QLORA_EINVAL;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lengths, 4) || !aligned(block_table, 4) ||

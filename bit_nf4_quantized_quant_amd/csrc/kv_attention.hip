@@ -5,8 +5,11 @@
 // fourth tile of 64 positions: a lane forms one position's score, and then
 // each lane sums its D / 64 elements over the tile.  The waves' running
 // maxima and sums are joined at the end.
-#include "common.h"
-#include "kv.h"
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include "kv_common.h"
 
 namespace qlora {
 namespace kv {
@@ -104,11 +107,37 @@ __global__ void __launch_bounds__(256) kv_attention_kernel(AttnArgs a, Nf4Table 
   if (a.lse && tid == 0) a.lse[token * a.q_heads + h] = L == 0.f ? -INFINITY : M + __logf(L);
 }
 
+// fp32 -> fp16 bits, round to nearest even, for magnitudes of fp16's normal range (or 0).
+uint32_t f16_bits(float f) {
+  uint32_t u;
+  std::memcpy(&u, &f, 4);
+  const uint32_t sign = (u >> 16) & 0x8000u;
+  u &= 0x7FFFFFFFu;
+  if (u == 0) return 0;
+  u += 0xFFFu + ((u >> 13) & 1u);
+  return sign | ((u >> 13) - (112u << 10));
+}
+
 }  // namespace
 
-size_t kv_attention_workspace_bytes(const AttnArgs&) { return 0; }
+const Levels& levels_of(int table) {
+  static Levels lv[kCodeTables];
+  static std::once_flag once;
+  std::call_once(once, [] {
+    for (int ty = 0; ty < kCodeTables; ++ty) {
+      // the uniform grid's levels are odd multiples of 1/15, FP4's are E2M1 numbers over 6
+      const float kappa = ty == kTableUniform4 ? 15.f : ty == kTableFp4 ? 3.f : 1.f;
+      lv[ty].inv_kappa = 1.0f / kappa;
+      for (int i = 0; i < 16; ++i) lv[ty].h[i] = f16_bits(kappa * code_table(ty).level[i]);
+    }
+  });
+  return lv[table];
+}
+
+size_t kv_attention_workspace_bytes(const AttnArgs& a) { return decode_fits(a) ? decode_workspace_bytes(a) : 0; }
 
 hipError_t launch_kv_attention(const AttnArgs& a, hipStream_t s) {
+  if (decode_fits(a)) return launch_decode(a, s);
   const dim3 grid((unsigned)a.max_q, (unsigned)a.q_heads, (unsigned)a.seqs);
   const Nf4Table& t = code_table(a.c.table);
   if (a.c.D == 64)

@@ -1,0 +1,151 @@
+// Shared pieces of the attention kernels over the 4-bit cache (gfx950).
+#pragma once
+
+#include "common.h"
+#include "kv.h"
+
+namespace qlora {
+namespace kv {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// The 16 levels as the matrix products take them: fp16(kappa level), with
+// kappa the table's smallest factor that makes every level an fp16 number (15
+// for the uniform grid, 3 for FP4: both enter exactly) and 1 for NF4, whose
+// quantiles fp16 holds to 2^-11.
+struct Levels {
+  uint32_t h[16];
+  float inv_kappa;
+};
+
+const Levels& levels_of(int table);   // host; built once
+
+// Attention for few query rows (kv_decode.hip).
+bool decode_fits(const AttnArgs& a);
+size_t decode_workspace_bytes(const AttnArgs& a);
+hipError_t launch_decode(const AttnArgs& a, hipStream_t s);
+
+// The queries of sequence b that a workgroup or a joining wave works on, and the
+// positions they see.  Row r of a head's queries is query r / group, head
+// r % group of the group.
+struct Seq {
+  int q0, n;       // first token, queries
+  int len;         // positions held by the table's pages
+  int64_t shift;   // query i stands at position shift + i
+};
+
+__device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
+  Seq s;
+  const int length = a.lengths[b];
+  if (a.q_starts) {
+    const int tokens = (int)a.tokens;
+    s.q0 = min(max(a.q_starts[b], 0), tokens);
+    s.n = min(min(max(a.q_starts[b + 1] - s.q0, 0), (int)a.max_q), tokens - s.q0);
+  } else {
+    s.q0 = b * (int)a.max_q;
+    s.n = (int)a.max_q;
+  }
+  s.len = min(max(length, 0), (int)a.table_width * (int)a.c.page_size);
+  s.shift = (int64_t)length - s.n;
+  return s;
+}
+
+// Positions [low, high) that query i sees.
+__device__ __forceinline__ int seen_high(const AttnArgs& a, const Seq& s, int i) {
+  const int64_t p = s.shift + i + 1;
+  return a.causal ? (int)max((int64_t)0, min((int64_t)s.len, p)) : s.len;
+}
+__device__ __forceinline__ int seen_low(const AttnArgs& a, const Seq& s, int i) {
+  return a.window > 0 ? (int)min((int64_t)s.len, max((int64_t)0, s.shift + i + 1 - a.window)) : 0;
+}
+
+// The positions a tile of query rows [r0, r1) works through, cut in splits of
+// `chunk`: from the first one's low end, rounded down to 16 rows of a page, to
+// the last one's high end.  The last split takes what is left.
+struct Span {
+  int low, high;
+};
+__device__ __forceinline__ Span tile_span(const AttnArgs& a, const Seq& s, int i_first, int i_last) {
+  Span p;
+  p.low = seen_low(a, s, i_first) & ~15;
+  p.high = seen_high(a, s, i_last);
+  return p;
+}
+__device__ __forceinline__ int live_splits(const Span& p, int chunk, int splits) {
+  return p.high <= p.low ? 0 : min(splits, (p.high - p.low + chunk - 1) / chunk);
+}
+
+// Joined over the four 16-lane rows of a wave (rows differ, lanes of a column agree after it).
+__device__ __forceinline__ float rows_max(float v) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float rows_add(float v) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// 2^e for -126 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  f16x2 v;
+  v[0] = (_Float16)lo;
+  v[1] = (_Float16)hi;
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// Pair table in LDS: entry e (a code byte) = the fp16 levels of its two codes,
+// at byte 256 e, 32 copies (one per lane % 32), so that the address
+// 256 byte + 4 (lane % 32) is one byte permute and the lanes of a half-wave
+// always hit distinct banks.  The upper half of each 256 bytes is free.
+constexpr int kPairBytes = 256 * 256;
+
+__device__ __forceinline__ uint32_t level_pair(const Levels& lv, uint32_t e) {
+  int tab = 0;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) asm volatile("v_writelane_b32 %0, %1, %2" : "+v"(tab) : "s"(lv.h[k]), "n"(k));
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute((int)((e & 15u) * 4u), tab);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute((int)((e >> 4) * 4u), tab);
+  return lo | (hi << 16);
+}
+
+// Thread t of `threads` (a multiple of 256) writes its share of entry t % 256's
+// eight 16-byte pieces, in a per-entry rotated order.
+template <int threads>
+__device__ __forceinline__ void build_pairs(const Levels& lv, char* lut) {
+  constexpr uint32_t per = 8 / (threads / 256);
+  const uint32_t e = threadIdx.x & 255, part = threadIdx.x >> 8;
+  const uint32_t pv = level_pair(lv, e);
+  u32x4* dst = reinterpret_cast<u32x4*>(lut + e * 256);
+#pragma unroll
+  for (uint32_t i = 0; i < per; ++i) dst[(per * part + i + e) & 7] = u32x4{pv, pv, pv, pv};
+}
+
+// The eight levels of a dword of codes, in order, as one matrix operand.
+// lane4 = 4 (lane % 32).
+__device__ __forceinline__ f16x8 expand8(const char* lut, uint32_t word, uint32_t lane4) {
+  u32x4 v;
+  v[0] = *reinterpret_cast<const uint32_t*>(lut + __builtin_amdgcn_perm(word, lane4, 0x0c0c0400u));
+  v[1] = *reinterpret_cast<const uint32_t*>(lut + __builtin_amdgcn_perm(word, lane4, 0x0c0c0500u));
+  v[2] = *reinterpret_cast<const uint32_t*>(lut + __builtin_amdgcn_perm(word, lane4, 0x0c0c0600u));
+  v[3] = *reinterpret_cast<const uint32_t*>(lut + __builtin_amdgcn_perm(word, lane4, 0x0c0c0700u));
+  return __builtin_bit_cast(f16x8, v);
+}
+
+// The bf16 number at index i of packed words, as fp32.
+__device__ __forceinline__ float bf16_at(const uint32_t* w, int i) { return (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); }
+
+}  // namespace kv
+}  // namespace qlora

@@ -1,0 +1,558 @@
+// Attention over the 4-bit key/value cache for few query rows (gfx950): single
+// tokens and short runs of them, up to a few dozen rows (queries x heads of the
+// group) on one kv head.
+//
+//   out_i = sum_j softmax_j(scale q_i k_j) v_j
+//
+// What bounds it is the cache's bytes: each row is read once from HBM and its
+// codes are expanded in registers, by way of a table of level pairs in LDS,
+// straight into fp16 matrix operands.  The scales never touch the operands: a
+// key's scales multiply the scores of its 64-element runs after the product, a
+// value's multiply the softmax weights before it.
+//
+// Split.  A workgroup takes one kv head, 16 kNQ query rows and a chunk of the
+// positions; its eight waves take tiles of 32 positions in turn, each with its
+// own running maximum and sum, and join over LDS at the end.  Where one chunk
+// does not cover the sequence the workgroups leave (maximum, sum, weighted
+// values) in the workspace and kv_join_kernel joins them.
+//
+// A tile in a wave.  Scores come out transposed, S^T = K Q^T by 16x16x32
+// products (rows are positions, columns are queries), so that a lane holds one
+// query's scores: the softmax needs two lane swaps for the maximum and none
+// for the weights, and the weights are already the second operand of
+// O^T = V^T P^T if the reduction axis is numbered to match.  V^T's operand
+// needs eight positions of one element in a lane; gfx950's transposing LDS
+// read of 4-bit data delivers that from the rows as they are stored.
+#include <algorithm>
+
+#include "kv_common.h"
+#include "launch.h"
+
+namespace qlora {
+namespace kv {
+namespace {
+
+constexpr int kWaves = 8;
+constexpr int kThreads = kWaves * 64;
+constexpr int kTile = 32;                       // positions per wave and step
+constexpr int kRound = kTile * kWaves;          // positions per workgroup and round
+constexpr int kMinEv = -100;                    // exponents of value scales below this count as this
+
+__device__ __forceinline__ f32x4 mfma16(const f16x8& a, const f16x8& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// One tile's cache rows on their way to a wave: two groups of 16 positions.
+template <int D>
+struct Tile {
+  static constexpr int NB = D / 64;
+  static constexpr int kScaleWords = 2 * NB;    // four positions' bf16 scales
+  static constexpr int kVPieces = D == 256 ? 2 : 1;
+  static constexpr int kVWords = D == 64 ? 2 : 4;
+  u32x2 k[2][NB];                               // [group][run]: 16 codes of position lane % 16
+  uint32_t v[2][kVPieces][kVWords];             // [group]: the group's rows, a lane's share in memory order
+  uint32_t ks[2][kScaleWords], vs[2][kScaleWords];   // positions 4 (lane / 16) .. + 3
+};
+
+template <int W>
+__device__ __forceinline__ void load_words(uint32_t (&dst)[W], const void* p) {
+  if constexpr (W == 2) {
+    const u32x2 w = *static_cast<const u32x2*>(p);
+    dst[0] = w[0], dst[1] = w[1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const u32x4 w = static_cast<const u32x4*>(p)[i / 4];
+      dst[i] = w[0], dst[i + 1] = w[1], dst[i + 2] = w[2], dst[i + 3] = w[3];
+    }
+  }
+}
+
+// row[g]: cache row of the group's first position (a wave-uniform number)
+template <int D>
+__device__ __forceinline__ void load_tile(Tile<D>& t, const Cache& c, const uint32_t (&row)[2], int lane) {
+  using T = Tile<D>;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const uint64_t at = (uint64_t)row[g] * (D / 2);
+    const uint8_t* k = c.codes[0] + at + (uint32_t)((lane & 15) * (D / 2) + (lane >> 4) * 8);
+#pragma unroll
+    for (int b = 0; b < T::NB; ++b) t.k[g][b] = *reinterpret_cast<const u32x2*>(k + b * 32);
+    const uint8_t* v = c.codes[1] + at + (uint32_t)(lane * T::kVWords * 4);
+#pragma unroll
+    for (int p = 0; p < T::kVPieces; ++p) load_words(t.v[g][p], v + p * 1024);
+    const uint64_t sat = (uint64_t)row[g] * T::NB;
+    load_words(t.ks[g], c.scales[0] + sat + (uint32_t)((lane >> 4) * 4 * T::NB));
+    load_words(t.vs[g], c.scales[1] + sat + (uint32_t)((lane >> 4) * 4 * T::NB));
+  }
+}
+
+// Where a wave keeps the value rows of a tile: 8-byte chunk `chunk` (16 codes)
+// of position pos (0..31), in the free upper halves of the pair table's
+// entries, 16 chunks per 128-byte piece.  The exclusive-or spreads the sixteen
+// chunks that 16 lanes read at once (eight positions, two chunks) over all banks.
+template <int D>
+__device__ __forceinline__ uint32_t v_at(int pos, int chunk) {
+  constexpr int kPer = D / 16;                  // chunks per row
+  constexpr int kRows = 16 / kPer;              // rows per piece
+  uint32_t slot;
+  if constexpr (D == 64)
+    slot = ((pos & 3) << 2) | (chunk ^ ((pos >> 4) << 1));
+  else if constexpr (D == 128)
+    slot = ((pos & 1) << 3) | (chunk ^ (pos & 2) ^ ((pos >> 4) << 2));
+  else
+    slot = chunk ^ ((pos & 3) << 1) ^ ((pos >> 4) << 3);
+  return (uint32_t)(pos / kRows) * 256 + 128 + slot * 8;
+}
+
+template <int D, int kNQ>
+struct Smem {
+  static constexpr int kPitch = 68;             // floats per row of the joining passes (64 + padding)
+  static constexpr size_t kJoin = (size_t)kWaves * 16 * kPitch * 4;
+  static constexpr size_t kStats = (size_t)kWaves * 16 * kNQ * 2 * 4;
+  static constexpr size_t kBytes = kPairBytes + kStats;
+  static_assert(kJoin <= kPairBytes, "the joining passes fit over the pair table");
+};
+
+struct Split {
+  int chunk, splits;   // positions per split, splits
+  int rows, tiles;     // query rows of a head at most, row tiles
+};
+
+// Where a split leaves row (token, head)'s partial result.
+struct Partial {
+  float* o;      // [rows][splits][D]
+  float2* stat;  // [rows][splits]: maximum, sum
+};
+
+template <int D, int kNQ>
+__global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
+    kv_decode_kernel(AttnArgs a, Split sp, Levels lv, Partial part) {
+  using T = Tile<D>;
+  constexpr int NB = D / 64, kRows = 16 * kNQ;
+  extern __shared__ __attribute__((aligned(256))) char smem[];
+  char* lut = smem;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, quad = lane >> 4;
+  const int split = blockIdx.x % sp.splits, b = blockIdx.y;
+  const int head = blockIdx.x / sp.splits / sp.tiles, r0 = blockIdx.x / sp.splits % sp.tiles * kRows;
+  const int group = (int)a.q_heads / (int)a.c.heads;
+  const Seq seq = sequence(a, b);
+  const int rows = seq.n * group;
+  if (r0 >= rows) return;
+  const int i_first = r0 / group, i_last = (min(r0 + kRows, rows) - 1) / group;
+  const Span span = tile_span(a, seq, i_first, i_last);
+  const int live = live_splits(span, sp.chunk, sp.splits);
+  if (split >= max(live, sp.splits == 1 ? 1 : 0)) return;
+  const int t0 = span.low + split * sp.chunk;
+  const int t1 = split == sp.splits - 1 ? span.high : min(span.high, t0 + sp.chunk);
+
+  // this wave's tiles are tiles wave, wave + 8, ... of the chunk; lane 2 k + g holds
+  // the cache row of group g of tile k of the next 32 of them, and a bit in `held`
+  // that its page exists
+  const int32_t* table = a.block_table + (int64_t)b * a.table_width;
+  auto find_rows = [&](int first, uint64_t& held) -> uint32_t {
+    const int t = t0 + ((first + (lane >> 1)) * kWaves + wave) * kTile + (lane & 1) * 16;
+    uint32_t row = 0;
+    bool ok = t < t1;
+    if (ok) {
+      const uint32_t pg = div_by((uint32_t)t, a.c.page_div);
+      const uint32_t page = (uint32_t)table[pg];
+      ok = page < a.c.pages;
+      if (ok) row = (page * a.c.heads + head) * a.c.page_size + ((uint32_t)t - pg * a.c.page_size);
+    }
+    held = __ballot(ok);
+    return row;
+  };
+  uint64_t held;
+  uint32_t found = find_rows(0, held);
+  auto tile_rows = [&](int k, uint32_t (&row)[2]) {
+    row[0] = __builtin_amdgcn_readlane(found, 2 * (k & 31));
+    row[1] = __builtin_amdgcn_readlane(found, 2 * (k & 31) + 1);
+  };
+  const int all = t1 > t0 ? (t1 - t0 + kTile - 1) / kTile : 0;
+  const int mine = all > wave ? (all - wave + kWaves - 1) / kWaves : 0;
+  Tile<D> cur;
+  uint32_t row[2];
+  if (mine > 0) {
+    tile_rows(0, row);
+    load_tile<D>(cur, a.c, row, lane);
+  }
+
+  // the queries: row r0 + 16 j + col of the head's, each divided by the power of
+  // two of its largest element so that fp16 holds it
+  f16x8 q[kNQ][NB][2];
+  float factor[kNQ];
+  int qlow[kNQ], qhigh[kNQ];
+#pragma unroll
+  for (int j = 0; j < kNQ; ++j) {
+    const int r = min(r0 + 16 * j + col, rows - 1), i = r / group;
+    qlow[j] = seen_low(a, seq, i);
+    qhigh[j] = seen_high(a, seq, i);
+    const uint16_t* src = a.q + (int64_t)(seq.q0 + i) * a.token_stride +
+                          (int64_t)(head * group + (r - i * group)) * a.head_stride + quad * 16;
+    u32x4 raw[NB][2];
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < NB; ++e)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        raw[e][w] = *reinterpret_cast<const u32x4*>(src + e * 64 + w * 8);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) top = max(top, max((raw[e][w][x] << 16) & 0x7FFFFFFFu, raw[e][w][x] & 0x7FFF0000u));
+      }
+    top = __float_as_uint(rows_max(__uint_as_float(min(top, 0x7E800000u))));
+    const int e2 = max((int)(top >> 23) - 127, -100);
+    const float down = pow2(-e2);
+#pragma unroll
+    for (int e = 0; e < NB; ++e)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        u32x4 h;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) h[x] = pack_f16x2(bf16_lo(raw[e][w][x]) * down, bf16_hi(raw[e][w][x]) * down);
+        q[j][e][w] = __builtin_bit_cast(f16x8, h);
+      }
+    factor[j] = a.scale * (kLog2e * lv.inv_kappa) * pow2(e2);
+  }
+  const int all_low = seen_low(a, seq, i_last), all_high = seen_high(a, seq, i_first);   // seen by every row
+
+  build_pairs<kThreads>(lv, lut);
+  __syncthreads();
+
+  const uint32_t lane4 = 4u * (lane & 31);
+  char* vbuf = lut + wave * (16 * 256);         // 16 pieces of 128 bytes (32 for D = 256, 8 for D = 64)
+  if constexpr (D == 256) vbuf = lut + wave * (32 * 256);
+  // the transposing reads: 16 lanes fetch eight positions (in the scores' order) x two chunks
+  const int tr_pos = (((lane & 7) >> 2) << 4) | (quad << 2) | (lane & 3), tr_sel = (lane >> 3) & 1;
+
+  f32x4 o[kNQ][4 * NB];
+  float m[kNQ], l[kNQ];                         // m: maximum of score + exponent of the tile's value scales
+#pragma unroll
+  for (int j = 0; j < kNQ; ++j) {
+    m[j] = -INFINITY, l[j] = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4 * NB; ++c) o[j][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  for (int k = 0; k < mine; ++k) {
+    const int pos0 = t0 + (k * kWaves + wave) * kTile;
+    const bool whole = pos0 >= all_low && pos0 + kTile <= min(all_high, t1) && ((held >> (2 * (k & 31))) & 3) == 3;
+    const uint32_t pages_ok = (uint32_t)(held >> (2 * (k & 31))) & 3u;
+    Tile<D> next;
+    if (k + 1 < mine) {
+      if (((k + 1) & 31) == 0) found = find_rows(k + 1, held);
+      tile_rows(k + 1, row);
+      load_tile<D>(next, a.c, row, lane);
+    }
+    // value rows into LDS
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int p = 0; p < T::kVPieces; ++p) {
+        if constexpr (D == 64) {
+          *reinterpret_cast<u32x2*>(vbuf + v_at<D>(16 * g + (lane >> 2), lane & 3)) = u32x2{cur.v[g][p][0], cur.v[g][p][1]};
+        } else {
+          const int pos = D == 128 ? lane >> 2 : p * 8 + (lane >> 3), chunk = 2 * (D == 128 ? lane & 3 : lane & 7);
+          *reinterpret_cast<u32x4*>(vbuf + v_at<D>(16 * g + pos, chunk)) =
+              u32x4{cur.v[g][p][0], cur.v[g][p][1], cur.v[g][p][2], cur.v[g][p][3]};
+        }
+      }
+    // scores: x[j][g][i] of position 16 g + 4 quad + i
+    float x[kNQ][2][4];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+#pragma unroll
+      for (int e = 0; e < NB; ++e) {
+        const f16x8 k0 = expand8(lut, cur.k[g][e][0], lane4), k1 = expand8(lut, cur.k[g][e][1], lane4);
+#pragma unroll
+        for (int j = 0; j < kNQ; ++j) {
+          f32x4 s = mfma16(k0, q[j][e][0], f32x4{0.f, 0.f, 0.f, 0.f});
+          s = mfma16(k1, q[j][e][1], s);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float ks = bf16_at(cur.ks[g], i * NB + e);
+            x[j][g][i] = e == 0 ? ks * s[i] : __builtin_fmaf(ks, s[i], x[j][g][i]);
+            if (e == NB - 1) x[j][g][i] *= factor[j];
+          }
+        }
+      }
+    }
+    if (!whole) {
+      // hidden positions: score -infinity.  A value scale goes to 0 where no row sees the
+      // position (stale rows), and where it is NaN, the scores of the rows that do see it
+      // turning NaN instead: 0 x NaN in the product would reach the rows that do not.
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int pos = pos0 + 16 * g + 4 * quad + i;
+          const bool there = pos < t1 && ((pages_ok >> g) & 1u);
+          bool bad = false;
+#pragma unroll
+          for (int e = 0; e < NB; ++e) {
+            const int w = i * NB + e;
+            const bool nan = !(fabsf(bf16_at(cur.vs[g], w)) < INFINITY);
+            bad = bad || nan;
+            if (nan || !there) cur.vs[g][w >> 1] &= (w & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+          }
+#pragma unroll
+          for (int j = 0; j < kNQ; ++j) {
+            if (bad) x[j][g][i] = NAN;
+            if (!(there && pos >= qlow[j] && pos < qhigh[j])) x[j][g][i] = -INFINITY;
+          }
+        }
+    }
+    // the largest value scale's exponent (bf16 patterns of positive numbers order like
+    // the numbers; + 0x40 turns NaN negative)
+    typedef short s16x2 __attribute__((ext_vector_type(2)));
+    s16x2 vm = {0, 0};
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int w = 0; w < T::kScaleWords; ++w)
+        vm = __builtin_elementwise_max(vm, __builtin_bit_cast(s16x2, cur.vs[g][w]) + s16x2{0x40, 0x40});
+    const float vtop = rows_max(__uint_as_float((uint32_t)max((int)max(vm[0], vm[1]) - 0x40, 0) << 16));
+    const int ev = min(max((int)(__builtin_amdgcn_readfirstlane(__float_as_uint(vtop)) >> 23) - 127, kMinEv), 126);
+    const float vdown = pow2(-ev), fev = (float)ev;
+#pragma unroll
+    for (int j = 0; j < kNQ; ++j) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, x[j][g][i]);
+      const float mn = fmaxf(m[j], rows_max(top) + fev);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      if (__any(mn > m[j])) {
+        const float alpha = exp2_fast(m[j] - ref);
+        l[j] *= alpha;
+#pragma unroll
+        for (int c = 0; c < 4 * NB; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[j][c][i] *= alpha;
+        m[j] = mn;
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[j][g][i] = exp2_fast(x[j][g][i] + (fev - ref));
+          sum += x[j][g][i];
+        }
+      l[j] = __builtin_fmaf(sum, vdown, l[j]);
+    }
+    // weights x value scales, as the second operand of each run's products
+    f16x8 pv[kNQ][NB];
+#pragma unroll
+    for (int e = 0; e < NB; ++e) {
+      float vs[2][4];
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vs[g][i] = bf16_at(cur.vs[g], i * NB + e) * vdown;
+#pragma unroll
+      for (int j = 0; j < kNQ; ++j) {
+        u32x4 h;
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int i = 0; i < 4; i += 2)
+            h[2 * g + i / 2] = pack_f16x2(x[j][g][i] * vs[g][i],
+                                          x[j][g][i + 1] * vs[g][i + 1]);
+        pv[j][e] = __builtin_bit_cast(f16x8, h);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4 * NB; c += 2) {
+      const i32x2 w = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+          (__attribute__((address_space(3))) i32x2*)(vbuf + v_at<D>(tr_pos, c + tr_sel)));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f16x8 v = expand8(lut, (uint32_t)w[h], lane4);
+#pragma unroll
+        for (int j = 0; j < kNQ; ++j) o[j][c + h] = mfma16(v, pv[j][(c + h) >> 2], o[j][c + h]);
+      }
+    }
+    cur = next;
+  }
+
+  // ---- join the eight waves
+  __syncthreads();                              // (the pair table is done with)
+  float2* stats = reinterpret_cast<float2*>(smem + kPairBytes);
+#pragma unroll
+  for (int j = 0; j < kNQ; ++j) {
+    l[j] = rows_add(l[j]);
+    if (quad == 0) stats[(wave * kNQ + j) * 16 + col] = make_float2(m[j], l[j]);
+  }
+  __syncthreads();
+  float* buf = reinterpret_cast<float*>(smem);
+  constexpr int P = Smem<D, kNQ>::kPitch;
+#pragma unroll
+  for (int j = 0; j < kNQ; ++j) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stats[(w * kNQ + j) * 16 + col].x);
+    const float f = exp2_fast(m[j] - (top == -INFINITY ? 0.f : top));
+    // the row a thread sums: row tid / 32, elements 2 (tid % 32) of each run
+    const int orow = tid >> 5, r = r0 + 16 * j + orow;
+    float rtop = -INFINITY, rsum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) rtop = fmaxf(rtop, stats[(w * kNQ + j) * 16 + orow].x);
+    const float rref = rtop == -INFINITY ? 0.f : rtop;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float2 s = stats[(w * kNQ + j) * 16 + orow];
+      rsum = __builtin_fmaf(exp2_fast(s.x - rref), s.y, rsum);
+    }
+    const int i = r / group;
+    const int64_t out_row = (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
+    const float inv = rsum == 0.f ? 0.f : lv.inv_kappa / rsum;
+#pragma unroll
+    for (int e = 0; e < NB; ++e) {
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        f32x4 v = o[j][4 * e + c];
+        v *= f;
+        *reinterpret_cast<f32x4*>(buf + (wave * 16 + col) * P + 16 * c + 4 * quad) = v;
+      }
+      __syncthreads();
+      float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float2 v = *reinterpret_cast<const float2*>(buf + (w * 16 + orow) * P + 2 * (tid & 31));
+        s.x += v.x, s.y += v.y;
+      }
+      if (r < rows) {
+        if (sp.splits == 1)
+          reinterpret_cast<uint32_t*>(a.out + out_row * D + e * 64)[tid & 31] = pack_bf16x2(s.x * inv, s.y * inv);
+        else
+          reinterpret_cast<float2*>(part.o + (out_row * sp.splits + split) * D + e * 64)[tid & 31] = s;
+      }
+    }
+    if (r < rows && (tid & 31) == 0) {
+      if (sp.splits > 1)
+        part.stat[out_row * sp.splits + split] = make_float2(rtop, rsum);
+      else if (a.lse)
+        a.lse[out_row] = rsum == 0.f ? -INFINITY : kLn2 * (rtop + __builtin_amdgcn_logf(rsum));
+    }
+  }
+}
+
+// Joins the splits of one row a wave.
+template <int D>
+__global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a, Split sp, int tile_rows, float inv_kappa, Partial part) {
+  constexpr int E = D / 64;
+  const int lane = threadIdx.x & 63;
+  const int group = (int)a.q_heads / (int)a.c.heads;
+  const int per = (sp.rows + 3) / 4;             // workgroups of four waves a head
+  const int r = blockIdx.x % per * 4 + (threadIdx.x >> 6), head = blockIdx.x / per, b = blockIdx.y;
+  const Seq seq = sequence(a, b);
+  const int rows = seq.n * group;
+  if (r >= rows) return;
+  const int r0 = r / tile_rows * tile_rows;
+  const Span span = tile_span(a, seq, r0 / group, (min(r0 + tile_rows, rows) - 1) / group);
+  const int live = live_splits(span, sp.chunk, sp.splits);
+  const int i = r / group;
+  const int64_t row = (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
+  const float2* stat = part.stat + row * sp.splits;
+  const float* o = part.o + row * sp.splits * D + lane * E;
+  float top = -INFINITY;
+  for (int s = lane; s < live; s += 64) top = fmaxf(top, stat[s].x);
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+  const float ref = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int s0 = 0; s0 < live; s0 += 64) {
+    float f = 0.f;
+    if (s0 + lane < live) {
+      const float2 st = stat[s0 + lane];
+      f = exp2_fast(st.x - ref);
+      sum = __builtin_fmaf(f, st.y, sum);
+    }
+    const int cnt = min(64, live - s0);
+#pragma unroll 4
+    for (int s = 0; s < cnt; ++s) {
+      const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s));
+      const float* src = o + (int64_t)(s0 + s) * D;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(fs, src[e], acc[e]);
+    }
+  }
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
+  const float inv = sum == 0.f ? 0.f : inv_kappa / sum;
+  uint16_t* out = a.out + row * D + lane * E;
+  if constexpr (E == 1) {
+    *out = (uint16_t)pack_bf16x2(acc[0] * inv, 0.f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; e += 2) reinterpret_cast<uint32_t*>(out)[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  }
+  if (a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : kLn2 * (top + __builtin_amdgcn_logf(sum));
+}
+
+// Few positions: one round of the eight waves.  Splits are otherwise sized so
+// that about kFill workgroups share the work.
+constexpr int kFill = 768;
+constexpr int kMaxSplits = 128;
+
+Split split_of(const AttnArgs& a, int tile_rows) {
+  Split s;
+  s.rows = (int)(a.max_q * (a.q_heads / a.c.heads));
+  s.tiles = (s.rows + tile_rows - 1) / tile_rows;
+  int64_t span = a.max_len;
+  if (a.window > 0) span = std::min(span, a.window + a.max_q + 15);
+  span = std::max<int64_t>(span, 1);
+  const int64_t groups = a.seqs * a.c.heads * s.tiles;
+  int64_t splits = std::max<int64_t>(1, kFill / groups);
+  splits = std::min<int64_t>(splits, kMaxSplits);
+  s.chunk = (int)std::max<int64_t>(kRound, (span + splits - 1) / splits + kRound - 1) / kRound * kRound;
+  s.splits = (int)((span + s.chunk - 1) / s.chunk);
+  return s;
+}
+
+int tile_rows_of(const AttnArgs& a) { return a.max_q * (a.q_heads / a.c.heads) <= 16 ? 16 : 32; }
+
+template <int D, int kNQ>
+hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Partial& part, hipStream_t s) {
+  const hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kv_decode_kernel<D, kNQ>), Smem<D, kNQ>::kBytes);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((kv_decode_kernel<D, kNQ>), dim3((unsigned)(sp.splits * sp.tiles * a.c.heads), (unsigned)a.seqs),
+                     dim3(kThreads), (Smem<D, kNQ>::kBytes), s, a, sp, lv, part);
+  if (sp.splits > 1)
+    hipLaunchKernelGGL(kv_join_kernel<D>, dim3((unsigned)((sp.rows + 3) / 4 * a.c.heads), (unsigned)a.seqs), dim3(256), 0,
+                       s, a, sp, 16 * kNQ, lv.inv_kappa, part);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool decode_fits(const AttnArgs& a) { return a.max_q * (a.q_heads / a.c.heads) <= 64; }
+
+size_t decode_workspace_bytes(const AttnArgs& a) {
+  const Split sp = split_of(a, tile_rows_of(a));
+  if (sp.splits == 1) return 0;
+  return (size_t)(a.tokens * a.q_heads) * sp.splits * (a.c.D * sizeof(float) + sizeof(float2));
+}
+
+hipError_t launch_decode(const AttnArgs& a, hipStream_t s) {
+  const int tile_rows = tile_rows_of(a);
+  const Split sp = split_of(a, tile_rows);
+  const Levels& lv = levels_of(a.c.table);
+  Partial part;
+  part.o = static_cast<float*>(a.workspace);
+  part.stat = reinterpret_cast<float2*>(part.o + (size_t)(a.tokens * a.q_heads) * sp.splits * a.c.D);
+  switch (a.c.D) {
+    case 64: return tile_rows == 16 ? launch<64, 1>(a, sp, lv, part, s) : launch<64, 2>(a, sp, lv, part, s);
+    case 128: return tile_rows == 16 ? launch<128, 1>(a, sp, lv, part, s) : launch<128, 2>(a, sp, lv, part, s);
+    default: return tile_rows == 16 ? launch<256, 1>(a, sp, lv, part, s) : launch<256, 2>(a, sp, lv, part, s);
+  }
+}
+
+}  // namespace kv
+}  // namespace qlora

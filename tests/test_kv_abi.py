@@ -107,6 +107,7 @@ def test_attention_workspace_is_asked_for():
     L = _lib.lib()
     size = L.qlora_kv_attention_workspace
     assert size(cache(), 3, 4, 4, 1, 32, 0) == 0 and size(cache(dim=96), 4, 4, 4, 1, 32, 0) == 0
+    assert size(cache(), 4, 0, 4, 1, 32, 0) == size(cache(), 4, 4, 0, 1, 32, 0) == size(cache(), 4, 4, 4, 0, 32, 0) == 0
     long = dict(tokens=1, seqs=1, max_len=1 << 20, width=1 << 16)
     need = size(cache(), 4, 1, 1, 1, 1 << 20, 0)
     if need:
