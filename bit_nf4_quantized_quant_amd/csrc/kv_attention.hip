@@ -1,10 +1,7 @@
-// Attention over the 4-bit key/value cache (gfx950):
-//   out_i = sum_j softmax_j(scale q_i k_j) v_j   over the positions j that query i sees.
-//
-// One workgroup a query row and head.  Each of its four waves takes every
-// fourth tile of 64 positions: a lane forms one position's score, and then
-// each lane sums its D / 64 elements over the tile.  The waves' running
-// maxima and sums are joined at the end.
+// Attention over the 4-bit key/value cache: the choice between the kernels for
+// few and for many query rows, the split of the positions, and the kernel that
+// joins the splits.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -15,96 +12,59 @@ namespace qlora {
 namespace kv {
 namespace {
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v = fmaxf(v, __shfl_xor(v, m));
-  return v;
-}
-__device__ __forceinline__ float wave_add(float v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-  return v;
-}
-
+// Joins the splits of one row a wave.
 template <int D>
-__global__ void __launch_bounds__(256) kv_attention_kernel(AttnArgs a, Nf4Table tab) {
-  constexpr int NB = D / 64;
-  __shared__ float lut[16];
-  __shared__ float qs[D];
-  __shared__ float om[4][D], mm[4], ll[4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int h = blockIdx.y, b = blockIdx.z, i = blockIdx.x;
-  const int64_t q0 = a.q_starts ? max(a.q_starts[b], 0) : (int64_t)b * a.max_q;
-  int64_t n = a.q_starts ? (int64_t)a.q_starts[b + 1] - q0 : a.max_q;
-  n = min(min(n, a.max_q), a.tokens - q0);
-  if (i >= n) return;
-  const int64_t token = q0 + i;
-  const int64_t len = min((int64_t)max(a.lengths[b], 0), a.table_width * a.c.page_size);
-  const int64_t pos = (int64_t)a.lengths[b] - n + i;
-  const int64_t hi = a.causal ? min(len, pos + 1) : len;
-  const int64_t lo = a.window > 0 ? max((int64_t)0, pos - a.window + 1) : 0;
-  if (tid < 16) lut[tid] = tab.level[tid];
-  if (tid < D) qs[tid] = __uint_as_float((uint32_t)a.q[token * a.token_stride + h * a.head_stride + tid] << 16) * a.scale;
-  __syncthreads();
-  const uint32_t head = h / (a.q_heads / a.c.heads);
-  float m = -INFINITY, l = 0.f, o[NB];
+__global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a, Split sp, float inv_kappa, Partial part) {
+  constexpr int E = D / 64;
+  const int lane = threadIdx.x & 63;
+  const int group = (int)a.q_heads / (int)a.c.heads;
+  const int per = (sp.rows + 3) / 4;             // workgroups of four waves a head
+  const int r = blockIdx.x % per * 4 + (threadIdx.x >> 6), head = blockIdx.x / per, b = blockIdx.y;
+  const Seq seq = sequence(a, b);
+  const int rows = seq.n * group;
+  if (r >= rows) return;
+  const int r0 = r / sp.tile_rows * sp.tile_rows;
+  const Span span = tile_span(a, seq, r0 / group, (min(r0 + sp.tile_rows, rows) - 1) / group);
+  const int live = live_splits(span, sp.chunk, sp.splits);
+  const int i = r / group;
+  const int64_t row = (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
+  const float2* stat = part.stat + row * sp.splits;
+  const float* o = part.o + row * sp.splits * D + lane * E;
+  float top = -INFINITY;
+  for (int s = lane; s < live; s += 64) top = fmaxf(top, stat[s].x);
 #pragma unroll
-  for (int e = 0; e < NB; ++e) o[e] = 0.f;
-  for (int64_t t0 = lo + 64 * wave; t0 < hi; t0 += 256) {
-    const int64_t t = t0 + lane;
-    const uint32_t tt = (uint32_t)(t < hi ? t : hi - 1);
-    const uint32_t pg = div_by(tt, a.c.page_div);
-    const int32_t page = a.block_table[b * a.table_width + pg];
-    const bool seen = t < hi && (uint32_t)page < a.c.pages;
-    const uint64_t row = (uint64_t)((seen ? page : 0) * a.c.heads + head) * a.c.page_size + (tt - pg * a.c.page_size);
-    float x = 0.f;
-    for (int blk = 0; blk < NB; ++blk) {
-      float part = 0.f;
-      for (int w = 0; w < 8; ++w) {
-        const uint32_t c = reinterpret_cast<const uint32_t*>(a.c.codes[0])[(row * NB + blk) * 8 + w];
+  for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+  const float ref = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, acc[E];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) part += lut[(c >> (4 * e)) & 15u] * qs[blk * 64 + w * 8 + e];
-      }
-      x += part * __uint_as_float((uint32_t)a.c.scales[0][row * NB + blk] << 16);
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int s0 = 0; s0 < live; s0 += 64) {
+    float f = 0.f;
+    if (s0 + lane < live) {
+      const float2 st = stat[s0 + lane];
+      f = exp2_fast(st.x - ref);
+      sum = __builtin_fmaf(f, st.y, sum);
     }
-    if (!seen) x = -INFINITY;
-    const float mn = fmaxf(m, wave_max(x));
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    const float alpha = __expf(m - ref), p = seen ? __expf(x - ref) : 0.f;
-    m = mn;
-    l = l * alpha + wave_add(p);
+    const int cnt = min(64, live - s0);
+#pragma unroll 4
+    for (int s = 0; s < cnt; ++s) {
+      const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s));
+      const float* src = o + (int64_t)(s0 + s) * D;
 #pragma unroll
-    for (int e = 0; e < NB; ++e) o[e] *= alpha;
-    const int cnt = (int)min((int64_t)64, hi - t0);
-    for (int j = 0; j < cnt; ++j) {
-      const uint64_t rj = (uint64_t)(uint32_t)__shfl((int)(uint32_t)row, j) |
-                          (uint64_t)(uint32_t)__shfl((int)(row >> 32), j) << 32;
-      const float pj = __shfl(p, j);
-      if (!__shfl((int)seen, j)) continue;
-#pragma unroll
-      for (int e = 0; e < NB; ++e) {
-        const uint32_t c = a.c.codes[1][rj * (D / 2) + e * 32 + (lane >> 1)];
-        const float v = lut[(lane & 1) ? c >> 4 : c & 15u] * __uint_as_float((uint32_t)a.c.scales[1][rj * NB + e] << 16);
-        o[e] += pj * v;
-      }
+      for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(fs, src[e], acc[e]);
     }
   }
 #pragma unroll
-  for (int e = 0; e < NB; ++e) om[wave][e * 64 + lane] = o[e];
-  if (lane == 0) mm[wave] = m, ll[wave] = l;
-  __syncthreads();
-  const float M = fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3]));
-  const float ref = M == -INFINITY ? 0.f : M;
-  float f[4], L = 0.f;
+  for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
+  const float inv = sum == 0.f ? 0.f : inv_kappa / sum;
+  uint16_t* out = a.out + row * D + lane * E;
+  if constexpr (E == 1) {
+    *out = (uint16_t)pack_bf16x2(acc[0] * inv, 0.f);
+  } else {
 #pragma unroll
-  for (int w = 0; w < 4; ++w) f[w] = __expf(mm[w] - ref), L += f[w] * ll[w];
-  if (tid < D) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) v += f[w] * om[w][tid];
-    a.out[(token * a.q_heads + h) * D + tid] = (uint16_t)pack_bf16x2(L > 0.f || L != L ? v / L : 0.f, 0.f);
+    for (int e = 0; e < E; e += 2) reinterpret_cast<uint32_t*>(out)[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
   }
-  if (a.lse && tid == 0) a.lse[token * a.q_heads + h] = L == 0.f ? -INFINITY : M + __logf(L);
+  if (a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : kLn2 * (top + __builtin_amdgcn_logf(sum));
 }
 
 // fp32 -> fp16 bits, round to nearest even, for magnitudes of fp16's normal range (or 0).
@@ -134,18 +94,46 @@ const Levels& levels_of(int table) {
   return lv[table];
 }
 
-size_t kv_attention_workspace_bytes(const AttnArgs& a) { return decode_fits(a) ? decode_workspace_bytes(a) : 0; }
+Split split_of(const AttnArgs& a, int tile_rows, int fill, int least) {
+  constexpr int kMaxSplits = 128;
+  Split s;
+  s.rows = (int)(a.max_q * (a.q_heads / a.c.heads));
+  s.tile_rows = tile_rows;
+  s.tiles = (s.rows + tile_rows - 1) / tile_rows;
+  int64_t span = a.max_len;
+  if (a.window > 0) span = std::min(span, a.window + a.max_q + 15);
+  span = std::max<int64_t>(span, 1);
+  const int64_t groups = a.seqs * a.c.heads * s.tiles;
+  const int64_t splits = std::min<int64_t>(std::max<int64_t>(1, fill / groups), kMaxSplits);
+  const int64_t each = std::max<int64_t>(least, (span + splits - 1) / splits);
+  s.chunk = (int)((each + least - 1) / least * least);
+  s.splits = (int)((span + s.chunk - 1) / s.chunk);
+  return s;
+}
+
+namespace {
+
+bool few_rows(const AttnArgs& a) { return a.max_q * (a.q_heads / a.c.heads) <= 64; }
+
+Split choose_split(const AttnArgs& a) { return few_rows(a) ? decode_split(a) : prompt_split(a); }
+
+}  // namespace
+
+size_t kv_attention_workspace_bytes(const AttnArgs& a) {
+  const Split sp = choose_split(a);
+  return sp.splits == 1 ? 0 : (size_t)(a.tokens * a.q_heads) * sp.splits * (a.c.D * sizeof(float) + sizeof(float2));
+}
 
 hipError_t launch_kv_attention(const AttnArgs& a, hipStream_t s) {
-  if (decode_fits(a)) return launch_decode(a, s);
-  const dim3 grid((unsigned)a.max_q, (unsigned)a.q_heads, (unsigned)a.seqs);
-  const Nf4Table& t = code_table(a.c.table);
-  if (a.c.D == 64)
-    hipLaunchKernelGGL(kv_attention_kernel<64>, grid, dim3(256), 0, s, a, t);
-  else if (a.c.D == 128)
-    hipLaunchKernelGGL(kv_attention_kernel<128>, grid, dim3(256), 0, s, a, t);
-  else
-    hipLaunchKernelGGL(kv_attention_kernel<256>, grid, dim3(256), 0, s, a, t);
+  const Split sp = choose_split(a);
+  Partial part;
+  part.o = static_cast<float*>(a.workspace);
+  part.stat = reinterpret_cast<float2*>(part.o + (size_t)(a.tokens * a.q_heads) * sp.splits * a.c.D);
+  const hipError_t e = few_rows(a) ? launch_decode(a, sp, part, s) : launch_prompt(a, sp, part, s);
+  if (e != hipSuccess || sp.splits == 1) return e;
+  const dim3 grid((unsigned)((sp.rows + 3) / 4 * a.c.heads), (unsigned)a.seqs);
+  const auto kernel = a.c.D == 64 ? kv_join_kernel<64> : a.c.D == 128 ? kv_join_kernel<128> : kv_join_kernel<256>;
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, sp, levels_of(a.c.table).inv_kappa, part);
   return hipGetLastError();
 }
 

@@ -25,10 +25,26 @@ struct Levels {
 
 const Levels& levels_of(int table);   // host; built once
 
-// Attention for few query rows (kv_decode.hip).
-bool decode_fits(const AttnArgs& a);
-size_t decode_workspace_bytes(const AttnArgs& a);
-hipError_t launch_decode(const AttnArgs& a, hipStream_t s);
+// How the positions of a row tile are cut, and where a split leaves the partial
+// result of row (token, head) if there are several.
+struct Split {
+  int chunk, splits;           // positions per split, splits
+  int rows, tiles, tile_rows;  // query rows of a head at most, row tiles, rows of one
+};
+struct Partial {
+  float* o;      // [rows][splits][D]
+  float2* stat;  // [rows][splits]: reference, sum
+};
+
+// Splits such that about `fill` workgroups share the work, of at least
+// `least` positions each (and a multiple of that).
+Split split_of(const AttnArgs& a, int tile_rows, int fill, int least);
+
+// Attention for few query rows (kv_decode.hip) and for many (kv_prompt.hip).
+Split decode_split(const AttnArgs& a);
+hipError_t launch_decode(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s);
+Split prompt_split(const AttnArgs& a);
+hipError_t launch_prompt(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s);
 
 // The queries of sequence b that a workgroup or a joining wave works on, and the
 // positions they see.  Row r of a head's queries is query r / group, head

@@ -114,17 +114,6 @@ struct Smem {
   static_assert(kJoin <= kPairBytes, "the joining passes fit over the pair table");
 };
 
-struct Split {
-  int chunk, splits;   // positions per split, splits
-  int rows, tiles;     // query rows of a head at most, row tiles
-};
-
-// Where a split leaves row (token, head)'s partial result.
-struct Partial {
-  float* o;      // [rows][splits][D]
-  float2* stat;  // [rows][splits]: maximum, sum
-};
-
 template <int D, int kNQ>
 __global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
     kv_decode_kernel(AttnArgs a, Split sp, Levels lv, Partial part) {
@@ -441,81 +430,6 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
   }
 }
 
-// Joins the splits of one row a wave.
-template <int D>
-__global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a, Split sp, int tile_rows, float inv_kappa, Partial part) {
-  constexpr int E = D / 64;
-  const int lane = threadIdx.x & 63;
-  const int group = (int)a.q_heads / (int)a.c.heads;
-  const int per = (sp.rows + 3) / 4;             // workgroups of four waves a head
-  const int r = blockIdx.x % per * 4 + (threadIdx.x >> 6), head = blockIdx.x / per, b = blockIdx.y;
-  const Seq seq = sequence(a, b);
-  const int rows = seq.n * group;
-  if (r >= rows) return;
-  const int r0 = r / tile_rows * tile_rows;
-  const Span span = tile_span(a, seq, r0 / group, (min(r0 + tile_rows, rows) - 1) / group);
-  const int live = live_splits(span, sp.chunk, sp.splits);
-  const int i = r / group;
-  const int64_t row = (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
-  const float2* stat = part.stat + row * sp.splits;
-  const float* o = part.o + row * sp.splits * D + lane * E;
-  float top = -INFINITY;
-  for (int s = lane; s < live; s += 64) top = fmaxf(top, stat[s].x);
-#pragma unroll
-  for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-  const float ref = top == -INFINITY ? 0.f : top;
-  float sum = 0.f, acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int s0 = 0; s0 < live; s0 += 64) {
-    float f = 0.f;
-    if (s0 + lane < live) {
-      const float2 st = stat[s0 + lane];
-      f = exp2_fast(st.x - ref);
-      sum = __builtin_fmaf(f, st.y, sum);
-    }
-    const int cnt = min(64, live - s0);
-#pragma unroll 4
-    for (int s = 0; s < cnt; ++s) {
-      const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s));
-      const float* src = o + (int64_t)(s0 + s) * D;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(fs, src[e], acc[e]);
-    }
-  }
-#pragma unroll
-  for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
-  const float inv = sum == 0.f ? 0.f : inv_kappa / sum;
-  uint16_t* out = a.out + row * D + lane * E;
-  if constexpr (E == 1) {
-    *out = (uint16_t)pack_bf16x2(acc[0] * inv, 0.f);
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; e += 2) reinterpret_cast<uint32_t*>(out)[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  }
-  if (a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : kLn2 * (top + __builtin_amdgcn_logf(sum));
-}
-
-// Few positions: one round of the eight waves.  Splits are otherwise sized so
-// that about kFill workgroups share the work.
-constexpr int kFill = 768;
-constexpr int kMaxSplits = 128;
-
-Split split_of(const AttnArgs& a, int tile_rows) {
-  Split s;
-  s.rows = (int)(a.max_q * (a.q_heads / a.c.heads));
-  s.tiles = (s.rows + tile_rows - 1) / tile_rows;
-  int64_t span = a.max_len;
-  if (a.window > 0) span = std::min(span, a.window + a.max_q + 15);
-  span = std::max<int64_t>(span, 1);
-  const int64_t groups = a.seqs * a.c.heads * s.tiles;
-  int64_t splits = std::max<int64_t>(1, kFill / groups);
-  splits = std::min<int64_t>(splits, kMaxSplits);
-  s.chunk = (int)std::max<int64_t>(kRound, (span + splits - 1) / splits + kRound - 1) / kRound * kRound;
-  s.splits = (int)((span + s.chunk - 1) / s.chunk);
-  return s;
-}
-
 int tile_rows_of(const AttnArgs& a) { return a.max_q * (a.q_heads / a.c.heads) <= 16 ? 16 : 32; }
 
 template <int D, int kNQ>
@@ -524,33 +438,20 @@ hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Pa
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((kv_decode_kernel<D, kNQ>), dim3((unsigned)(sp.splits * sp.tiles * a.c.heads), (unsigned)a.seqs),
                      dim3(kThreads), (Smem<D, kNQ>::kBytes), s, a, sp, lv, part);
-  if (sp.splits > 1)
-    hipLaunchKernelGGL(kv_join_kernel<D>, dim3((unsigned)((sp.rows + 3) / 4 * a.c.heads), (unsigned)a.seqs), dim3(256), 0,
-                       s, a, sp, 16 * kNQ, lv.inv_kappa, part);
   return hipGetLastError();
 }
 
 }  // namespace
 
-bool decode_fits(const AttnArgs& a) { return a.max_q * (a.q_heads / a.c.heads) <= 64; }
+Split decode_split(const AttnArgs& a) { return split_of(a, tile_rows_of(a), 768, kRound); }
 
-size_t decode_workspace_bytes(const AttnArgs& a) {
-  const Split sp = split_of(a, tile_rows_of(a));
-  if (sp.splits == 1) return 0;
-  return (size_t)(a.tokens * a.q_heads) * sp.splits * (a.c.D * sizeof(float) + sizeof(float2));
-}
-
-hipError_t launch_decode(const AttnArgs& a, hipStream_t s) {
-  const int tile_rows = tile_rows_of(a);
-  const Split sp = split_of(a, tile_rows);
+hipError_t launch_decode(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s) {
   const Levels& lv = levels_of(a.c.table);
-  Partial part;
-  part.o = static_cast<float*>(a.workspace);
-  part.stat = reinterpret_cast<float2*>(part.o + (size_t)(a.tokens * a.q_heads) * sp.splits * a.c.D);
+  const bool one = sp.tile_rows == 16;
   switch (a.c.D) {
-    case 64: return tile_rows == 16 ? launch<64, 1>(a, sp, lv, part, s) : launch<64, 2>(a, sp, lv, part, s);
-    case 128: return tile_rows == 16 ? launch<128, 1>(a, sp, lv, part, s) : launch<128, 2>(a, sp, lv, part, s);
-    default: return tile_rows == 16 ? launch<256, 1>(a, sp, lv, part, s) : launch<256, 2>(a, sp, lv, part, s);
+    case 64: return one ? launch<64, 1>(a, sp, lv, part, s) : launch<64, 2>(a, sp, lv, part, s);
+    case 128: return one ? launch<128, 1>(a, sp, lv, part, s) : launch<128, 2>(a, sp, lv, part, s);
+    default: return one ? launch<256, 1>(a, sp, lv, part, s) : launch<256, 2>(a, sp, lv, part, s);
   }
 }
 

@@ -1,0 +1,385 @@
+// Attention over the 4-bit key/value cache for many query rows (gfx950):
+// prompts, chunks of prompts, and large head groups.
+//
+//   out_i = sum_j softmax_j(scale q_i k_j) v_j
+//
+// What bounds it is the matrix cores together with the vector work of the
+// softmax.  A workgroup takes 256 query rows (queries x heads of the group) of
+// one kv head, 32 per wave, and walks the positions in tiles of 8192 / D.  The
+// codes of a tile are expanded once per workgroup, while the tile before it is
+// worked on: each wave turns an eighth of the keys and of the values into fp16
+// operands (level x scale, the scales divided by the power of two of the
+// tile's largest, which multiplies the scores and the weights instead) and
+// puts them in LDS in the order in which the products read them, 16 bytes a
+// lane.  The two buffers take 64 KiB, the table of level pairs another 64 KiB.
+//
+// As with few rows, S^T = K Q^T (32x32x16 products: rows are positions, columns
+// are queries) leaves a lane with one query's scores, and the weights enter
+// O^T = V^T P^T from the registers they were formed in, the positions of a
+// reduction step numbered to match.
+#include <algorithm>
+
+#include "kv_common.h"
+#include "launch.h"
+
+namespace qlora {
+namespace kv {
+namespace {
+
+constexpr int kWaves = 8;
+constexpr int kThreads = kWaves * 64;
+constexpr int kRows = 32 * kWaves;              // query rows per workgroup
+constexpr int kMinExp = -100;                   // exponents of a tile's largest scales below this count as this
+constexpr float kSlack = 8.f;                   // the maximum is brought up to date once it is off by 2^8
+
+__device__ __forceinline__ f32x16 mfma32(const f16x8& a, const f16x8& b, const f32x16& c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+template <int D>
+struct Shape {
+  static constexpr int NB = D / 64;             // scales per row
+  static constexpr int kTile = 8192 / D;        // positions per tile
+  static constexpr int NP = kTile / 32;         // 32-position parts of a tile
+  static constexpr int NU = D / 32;             // 32-element parts of a row (NP NU = 8 waves)
+  static constexpr int NS = D / 16;             // reduction steps of a score
+  static constexpr int kOperand = 16384;        // bytes of a tile's fp16 keys, or values
+  static constexpr int kRawOff = kPairBytes + 4 * kOperand;
+  static constexpr int kScaleOff = kRawOff + kWaves * 512;
+  static constexpr size_t kBytes = kScaleOff + kWaves * 512;
+};
+
+// Where one lane finds its share of a tile.
+struct Rows {
+  uint32_t code, scale;   // cache rows of the position whose codes, and whose scales, it loads
+  bool ok;                // the scales' positions are there (two of them for D = 64: bit 0 and bit 1)
+  bool ok2;
+};
+struct Raw {
+  u32x2 k, v;             // 16 codes each
+  uint32_t ks, vs;        // two scales each
+  bool ok, ok2;
+};
+
+__device__ __forceinline__ float half_max(float v) {   // over a wave's two halves
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_add(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// The largest of the wave's finite bf16 numbers (two a lane), as its exponent.
+__device__ __forceinline__ int top_exponent(uint32_t pair) {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  const s16x2 p = __builtin_bit_cast(s16x2, pair) + s16x2{0x40, 0x40};   // NaN turns negative
+  int v = max((int)max(p[0], p[1]), 0x40);
+  v = max(v, __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, false));
+  auto r = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
+  v = max((int)r[0], (int)r[1]);
+  r = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
+  v = __builtin_amdgcn_readfirstlane(max((int)r[0], (int)r[1])) - 0x40;
+  return min(max((v >> 7) - 127, kMinExp), 126);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+    kv_prompt_kernel(AttnArgs a, Split sp, Levels lv, Partial part) {
+  using S = Shape<D>;
+  constexpr int NB = S::NB, NP = S::NP, NU = S::NU, NS = S::NS, kTile = S::kTile;
+  extern __shared__ __attribute__((aligned(256))) char smem[];
+  char* lut = smem;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 31, half = lane >> 5;
+  const int split = blockIdx.x % sp.splits, b = blockIdx.y;
+  // the last row tiles of a causal prompt see most: they start first
+  const int rest = blockIdx.x / sp.splits;
+  const int head = rest % (int)a.c.heads, r0 = (sp.tiles - 1 - rest / (int)a.c.heads) * kRows;
+  const int group = (int)a.q_heads / (int)a.c.heads;
+  const Seq seq = sequence(a, b);
+  const int rows = seq.n * group;
+  if (r0 >= rows) return;
+  const Span span = tile_span(a, seq, r0 / group, (min(r0 + kRows, rows) - 1) / group);
+  const int live = live_splits(span, sp.chunk, sp.splits);
+  if (split >= max(live, sp.splits == 1 ? 1 : 0)) return;
+  const int t0 = span.low + split * sp.chunk;
+  const int t1 = split == sp.splits - 1 ? span.high : min(span.high, t0 + sp.chunk);
+  const int tiles = t1 > t0 ? (t1 - t0 + kTile - 1) / kTile : 0;
+
+  // ---- the queries of this wave: row w0 + col
+  const int w0 = r0 + 32 * wave;
+  const bool active = w0 < rows;
+  const int r = min(w0 + col, rows - 1), qi = r / group;
+  const int qlow = seen_low(a, seq, qi), qhigh = seen_high(a, seq, qi);
+  // positions that some, and that all, of the wave's rows see
+  const int i_first = min(w0, rows - 1) / group, i_last = (min(w0 + 32, rows) - 1) / group;
+  const int any_low = seen_low(a, seq, i_first), any_high = active ? seen_high(a, seq, i_last) : 0;
+  const int all_low = seen_low(a, seq, i_last), all_high = seen_high(a, seq, i_first);
+  const int64_t out_row = (int64_t)(seq.q0 + qi) * a.q_heads + head * group + (r - qi * group);
+  f16x8 q[NS];                                  // step s: elements 32 (s / 2) + 16 half + 8 (s % 2) ..
+  float factor;
+  {
+    const uint16_t* src = a.q + (int64_t)(seq.q0 + qi) * a.token_stride +
+                          (int64_t)(head * group + (r - qi * group)) * a.head_stride + half * 16;
+    u32x4 raw[NS];
+    uint32_t top = 0;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      raw[s] = *reinterpret_cast<const u32x4*>(src + 32 * (s >> 1) + 8 * (s & 1));
+#pragma unroll
+      for (int x = 0; x < 4; ++x) top = max(top, max((raw[s][x] << 16) & 0x7FFFFFFFu, raw[s][x] & 0x7FFF0000u));
+    }
+    top = __float_as_uint(half_max(__uint_as_float(min(top, 0x7E800000u))));
+    const int e2 = max((int)(top >> 23) - 127, -100);
+    // the sign of the score's factor goes into the queries, so that larger products are
+    // larger scores
+    const float down = a.scale > 0.f ? pow2(-e2) : a.scale < 0.f ? -pow2(-e2) : 0.f;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      u32x4 h;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) h[x] = pack_f16x2(bf16_lo(raw[s][x]) * down, bf16_hi(raw[s][x]) * down);
+      q[s] = __builtin_bit_cast(f16x8, h);
+    }
+    factor = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * (kLog2e * lv.inv_kappa) * pow2(e2);
+  }
+
+  // ---- a tile's way into LDS
+  const int32_t* table = a.block_table + (int64_t)b * a.table_width;
+  const int wp = wave / NU, wu = wave % NU;     // this wave's part of the positions and of the elements
+  auto row_of = [&](int t, bool& ok) -> uint32_t {
+    ok = t < t1;
+    uint32_t row = 0;
+    if (ok) {
+      const uint32_t pg = div_by((uint32_t)t, a.c.page_div);
+      const uint32_t page = (uint32_t)table[pg];
+      ok = page < a.c.pages;
+      if (ok) row = (page * a.c.heads + head) * a.c.page_size + ((uint32_t)t - pg * a.c.page_size);
+    }
+    return row;
+  };
+  auto find = [&](int k) -> Rows {
+    Rows f;
+    bool unused;
+    f.code = row_of(t0 + k * kTile + 32 * wp + col, unused);
+    const int st = t0 + k * kTile + (D == 64 ? 2 * lane : D == 128 ? lane : lane >> 1);
+    f.scale = row_of(st, f.ok);
+    f.ok2 = D == 64 ? f.ok && st + 1 < t1 : f.ok;
+    return f;
+  };
+  auto load = [&](const Rows& f) -> Raw {
+    Raw w;
+    const uint64_t at = (uint64_t)f.code * (D / 2) + (uint32_t)(wu * 16 + half * 8);
+    w.k = *reinterpret_cast<const u32x2*>(a.c.codes[0] + at);
+    w.v = *reinterpret_cast<const u32x2*>(a.c.codes[1] + at);
+    const uint64_t sat = (uint64_t)f.scale * NB + (D == 256 ? 2 * (lane & 1) : 0);
+    w.ks = *reinterpret_cast<const uint32_t*>(a.c.scales[0] + sat);
+    w.vs = *reinterpret_cast<const uint32_t*>(a.c.scales[1] + sat);
+    w.ok = f.ok, w.ok2 = f.ok2;
+    return w;
+  };
+  const uint32_t lane4 = 4u * (lane & 31);
+  char* raw_v = smem + S::kRawOff + wave * 512;
+  // [position][run] of the keys, then [run][position] of the values, fp16
+  _Float16* ks_tab = reinterpret_cast<_Float16*>(smem + S::kScaleOff + wave * 512);
+  _Float16* vs_tab = ks_tab + 128;
+  // a tile's exponents and whether all of its positions are there, the same in every wave
+  struct Meta {
+    int ek, ev;
+    bool full;
+  };
+  auto stage = [&](Raw w, int buf) -> Meta {
+    Meta meta;
+    meta.full = __all(w.ok && w.ok2);
+    const uint32_t keep = (w.ok ? 0xFFFFu : 0u) | (w.ok2 ? 0xFFFF0000u : 0u);
+    w.ks &= keep, w.vs &= keep;
+    meta.ek = top_exponent(w.ks);
+    meta.ev = top_exponent(w.vs);
+    const float kd = pow2(-meta.ek), vd = pow2(-meta.ev);
+    float k0 = bf16_lo(w.ks) * kd, k1 = bf16_hi(w.ks) * kd, v0 = bf16_lo(w.vs) * vd, v1 = bf16_hi(w.vs) * vd;
+    // a value scale that is not finite turns its position's scores NaN instead of the
+    // value: 0 x NaN in the product would reach the rows that do not see the position
+    const bool bad0 = !(fabsf(v0) < INFINITY), bad1 = !(fabsf(v1) < INFINITY);
+    if (bad0) v0 = 0.f, k0 = NAN;
+    if (bad1) v1 = 0.f, k1 = NAN;
+    *reinterpret_cast<f16x2*>(ks_tab + 2 * lane) = f16x2{(_Float16)k0, (_Float16)k1};
+    if constexpr (D == 64) {
+      *reinterpret_cast<f16x2*>(vs_tab + 2 * lane) = f16x2{(_Float16)v0, (_Float16)v1};
+    } else {
+      const int pos = D == 128 ? lane : lane >> 1, run = D == 128 ? 0 : 2 * (lane & 1);
+      vs_tab[run * kTile + pos] = (_Float16)v0;
+      vs_tab[(run + 1) * kTile + pos] = (_Float16)v1;
+    }
+    *reinterpret_cast<u32x2*>(raw_v + lane * 8) = w.v;      // [chunk][position] of 16 codes each
+    char* kbuf = smem + kPairBytes + buf * (2 * S::kOperand);
+    char* vbuf = kbuf + S::kOperand;
+    const _Float16 ks = ks_tab[(32 * wp + col) * NB + (wu >> 1)];
+    const f16x8 ks8 = {ks, ks, ks, ks, ks, ks, ks, ks};
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      *reinterpret_cast<f16x8*>(kbuf + ((wp * NS + 2 * wu + x) * 64 + lane) * 16) = expand8(lut, w.k[x], lane4) * ks8;
+    // values: 16 lanes fetch 16 positions of their 16 elements, in the order of the scores
+    const int tr_pos = ((lane >> 3) & 1) * 16 + ((lane >> 2) & 1) * 8 + half * 4 + (lane & 3);
+    const i32x2 t = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+        (__attribute__((address_space(3))) i32x2*)(raw_v + (((lane >> 4) & 1) * 32 + tr_pos) * 8));
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const _Float16* vs = vs_tab + (wu >> 1) * kTile + 32 * wp + 16 * x + 4 * half;
+      const u32x2 lo = *reinterpret_cast<const u32x2*>(vs), hi = *reinterpret_cast<const u32x2*>(vs + 8);
+      const f16x8 vs8 = __builtin_bit_cast(f16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
+      *reinterpret_cast<f16x8*>(vbuf + (((wu * NP + wp) * 2 + x) * 64 + lane) * 16) =
+          expand8(lut, (uint32_t)t[x], lane4) * vs8;
+    }
+    return meta;
+  };
+
+  build_pairs<kThreads>(lv, lut);
+  Rows found = find(0);
+  Raw raw = load(found);
+  found = find(1);
+  __syncthreads();
+  Meta meta{0, 0, false};
+  if (tiles > 0) meta = stage(raw, 0);
+  raw = load(found);
+  found = find(2);
+  __syncthreads();
+
+  f32x16 o[NU];
+#pragma unroll
+  for (int u = 0; u < NU; ++u)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[u][i] = 0.f;
+  float m = -INFINITY, l = 0.f;                 // m: reference of score + exponent of the tile's value scales
+
+  for (int k = 0; k < tiles; ++k) {
+    const Raw next = load(found);
+    found = find(k + 3);
+    const int pos0 = t0 + k * kTile;
+    const Meta now = meta;
+    if (pos0 < any_high && pos0 + kTile > any_low) {
+      const char* kbuf = smem + kPairBytes + (k & 1) * (2 * S::kOperand);
+      const char* vbuf = kbuf + S::kOperand;
+      f32x16 s[NP];
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[p][i] = 0.f;
+#pragma unroll
+      for (int x = 0; x < NS; ++x)
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+          s[p] = mfma32(*reinterpret_cast<const f16x8*>(kbuf + ((p * NS + x) * 64 + lane) * 16), q[x], s[p]);
+      if (!(now.full && pos0 >= all_low && pos0 + kTile <= all_high)) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          uint32_t ok = 0xFFFFFFFFu;
+          if (!now.full) {                      // which positions are there: 16 share a page
+            bool here;
+            row_of(pos0 + 32 * p + col, here);
+            ok = (uint32_t)__ballot(here);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int at = 8 * (i >> 2) + 4 * half + (i & 3), pos = pos0 + 32 * p + at;
+            if (!(pos >= qlow && pos < qhigh && ((ok >> at) & 1u))) s[p][i] = -INFINITY;
+          }
+        }
+      }
+      const float cf = factor * pow2(now.ek), fev = (float)now.ev;
+      float top = -INFINITY;
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[p][i]);
+      const float mn = __builtin_fmaf(half_max(top), cf, fev);
+      if (__any(mn > m + kSlack)) {
+        const float up = fmaxf(m, mn);
+        const float alpha = exp2_fast(m - (up == -INFINITY ? 0.f : up));
+        l *= alpha;
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[u][i] *= alpha;
+        m = up;
+      }
+      const float base = fev - (m == -INFINITY ? 0.f : m);
+      float sum = 0.f;
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[p][i] = exp2_fast(__builtin_fmaf(s[p][i], cf, base));
+          sum += s[p][i];
+        }
+      l = __builtin_fmaf(sum, pow2(-now.ev), l);
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          u32x4 h;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = pack_f16x2(s[p][8 * x + 2 * i], s[p][8 * x + 2 * i + 1]);
+          const f16x8 w = __builtin_bit_cast(f16x8, h);
+#pragma unroll
+          for (int u = 0; u < NU; ++u)
+            o[u] = mfma32(*reinterpret_cast<const f16x8*>(vbuf + (((u * NP + p) * 2 + x) * 64 + lane) * 16), w, o[u]);
+        }
+    }
+    if (k + 1 < tiles) meta = stage(raw, (k + 1) & 1);
+    raw = next;
+    __syncthreads();
+  }
+
+  // ---- out: lane (col, half) holds elements 32 u + 8 x + 4 half .. + 3 of row w0 + col
+  l = half_add(l);
+  if (w0 + col >= rows) return;
+  if (sp.splits > 1) {
+    float* dst = part.o + (out_row * sp.splits + split) * D + 4 * half;
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        *reinterpret_cast<f32x4*>(dst + 32 * u + 8 * x) =
+            f32x4{o[u][4 * x], o[u][4 * x + 1], o[u][4 * x + 2], o[u][4 * x + 3]};
+    if (half == 0) part.stat[out_row * sp.splits + split] = make_float2(m, l);
+  } else {
+    const float inv = l == 0.f ? 0.f : lv.inv_kappa / l;
+    uint16_t* dst = a.out + out_row * D + 4 * half;
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        *reinterpret_cast<u32x2*>(dst + 32 * u + 8 * x) = u32x2{pack_bf16x2(o[u][4 * x] * inv, o[u][4 * x + 1] * inv),
+                                                                pack_bf16x2(o[u][4 * x + 2] * inv, o[u][4 * x + 3] * inv)};
+    if (a.lse && half == 0) a.lse[out_row] = l == 0.f ? -INFINITY : kLn2 * (m + __builtin_amdgcn_logf(l));
+  }
+}
+
+template <int D>
+hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Partial& part, hipStream_t s) {
+  const hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kv_prompt_kernel<D>), Shape<D>::kBytes);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kv_prompt_kernel<D>, dim3((unsigned)(sp.splits * sp.tiles * a.c.heads), (unsigned)a.seqs),
+                     dim3(kThreads), Shape<D>::kBytes, s, a, sp, lv, part);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// One workgroup fills a CU: the positions are split where there are fewer.
+Split prompt_split(const AttnArgs& a) { return split_of(a, kRows, 256, 512); }
+
+hipError_t launch_prompt(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s) {
+  const Levels& lv = levels_of(a.c.table);
+  switch (a.c.D) {
+    case 64: return launch<64>(a, sp, lv, part, s);
+    case 128: return launch<128>(a, sp, lv, part, s);
+    default: return launch<256>(a, sp, lv, part, s);
+  }
+}
+
+}  // namespace kv
+}  // namespace qlora
