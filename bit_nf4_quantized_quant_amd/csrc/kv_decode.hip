@@ -26,7 +26,6 @@
 #include <algorithm>
 
 #include "kv_common.h"
-#include "launch.h"
 
 namespace qlora {
 namespace kv {
@@ -37,6 +36,7 @@ constexpr int kThreads = kWaves * 64;
 constexpr int kTile = 32;                       // positions per wave and step
 constexpr int kRound = kTile * kWaves;          // positions per workgroup and round
 constexpr int kMinEv = -100;                    // exponents of value scales below this count as this
+constexpr float kSlack = 8.f;                   // the reference is brought up to date once it is off by 2^8
 
 __device__ __forceinline__ f32x4 mfma16(const f16x8& a, const f16x8& b, const f32x4& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -55,36 +55,50 @@ struct Tile {
 };
 
 template <int W>
-__device__ __forceinline__ void load_words(uint32_t (&dst)[W], const void* p) {
+__device__ __forceinline__ void load_words(uint32_t (&dst)[W], const rsrc_t& rs, uint32_t off) {
   if constexpr (W == 2) {
-    const u32x2 w = *static_cast<const u32x2*>(p);
+    const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0));
     dst[0] = w[0], dst[1] = w[1];
   } else {
 #pragma unroll
     for (int i = 0; i < W; i += 4) {
-      const u32x4 w = static_cast<const u32x4*>(p)[i / 4];
+      const u32x4 w = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off + 4 * i, 0, 0));
       dst[i] = w[0], dst[i + 1] = w[1], dst[i + 2] = w[2], dst[i + 3] = w[3];
     }
   }
 }
 
-// row[g]: cache row of the group's first position (a wave-uniform number)
+// Loads of a tile's parts; row[g]: cache row of the group's first position (a
+// wave-uniform number).  Each part is loaded again for the next tile as soon as
+// this tile is done with it, so one set of registers is enough.
 template <int D>
-__device__ __forceinline__ void load_tile(Tile<D>& t, const Cache& c, const uint32_t (&row)[2], int lane) {
-  using T = Tile<D>;
+__device__ __forceinline__ void load_keys(Tile<D>& t, const Cache& c, const uint32_t (&row)[2], int lane) {
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const uint64_t at = (uint64_t)row[g] * (D / 2);
-    const uint8_t* k = c.codes[0] + at + (uint32_t)((lane & 15) * (D / 2) + (lane >> 4) * 8);
+    const rsrc_t k = make_rsrc(c.codes[0] + (uint64_t)row[g] * (D / 2), 16 * (D / 2));
 #pragma unroll
-    for (int b = 0; b < T::NB; ++b) t.k[g][b] = *reinterpret_cast<const u32x2*>(k + b * 32);
-    const uint8_t* v = c.codes[1] + at + (uint32_t)(lane * T::kVWords * 4);
-#pragma unroll
-    for (int p = 0; p < T::kVPieces; ++p) load_words(t.v[g][p], v + p * 1024);
-    const uint64_t sat = (uint64_t)row[g] * T::NB;
-    load_words(t.ks[g], c.scales[0] + sat + (uint32_t)((lane >> 4) * 4 * T::NB));
-    load_words(t.vs[g], c.scales[1] + sat + (uint32_t)((lane >> 4) * 4 * T::NB));
+    for (int b = 0; b < Tile<D>::NB; ++b)
+      t.k[g][b] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(
+                                                k, (uint32_t)((lane & 15) * (D / 2) + (lane >> 4) * 8 + b * 32), 0, 0));
   }
+}
+template <int D>
+__device__ __forceinline__ void load_values(Tile<D>& t, const Cache& c, const uint32_t (&row)[2], int lane) {
+  using T = Tile<D>;
+#pragma unroll
+  for (int g = 0; g < 2; ++g)
+#pragma unroll
+    for (int p = 0; p < T::kVPieces; ++p)
+      load_words(t.v[g][p], make_rsrc(c.codes[1] + (uint64_t)row[g] * (D / 2), 16 * (D / 2)),
+                 (uint32_t)(lane * T::kVWords * 4 + p * 1024));
+}
+template <int D>
+__device__ __forceinline__ void load_scales(uint32_t (&w)[2][Tile<D>::kScaleWords], const uint16_t* scales,
+                                            const uint32_t (&row)[2], int lane) {
+  constexpr int NB = Tile<D>::NB;
+#pragma unroll
+  for (int g = 0; g < 2; ++g)
+    load_words(w[g], make_rsrc(scales + (uint64_t)row[g] * NB, 16 * NB * 2), (uint32_t)((lane >> 4) * 8 * NB));
 }
 
 // Where a wave keeps the value rows of a tile: 8-byte chunk `chunk` (16 codes)
@@ -119,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
     kv_decode_kernel(AttnArgs a, Split sp, Levels lv, Partial part) {
   using T = Tile<D>;
   constexpr int NB = D / 64, kRows = 16 * kNQ;
-  extern __shared__ __attribute__((aligned(256))) char smem[];
+  __shared__ __attribute__((aligned(256))) char smem[Smem<D, kNQ>::kBytes];
   char* lut = smem;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, quad = lane >> 4;
@@ -163,10 +177,11 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
   const int mine = all > wave ? (all - wave + kWaves - 1) / kWaves : 0;
   Tile<D> cur;
   uint32_t row[2];
-  if (mine > 0) {
-    tile_rows(0, row);
-    load_tile<D>(cur, a.c, row, lane);
-  }
+  tile_rows(0, row);                            // (row 0 of the cache where there is no tile)
+  load_values<D>(cur, a.c, row, lane);
+  load_keys<D>(cur, a.c, row, lane);
+  load_scales<D>(cur.ks, a.c.scales[0], row, lane);
+  load_scales<D>(cur.vs, a.c.scales[1], row, lane);
 
   // the queries: row r0 + 16 j + col of the head's, each divided by the power of
   // two of its largest element so that fp16 holds it
@@ -192,7 +207,9 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
       }
     top = __float_as_uint(rows_max(__uint_as_float(min(top, 0x7E800000u))));
     const int e2 = max((int)(top >> 23) - 127, -100);
-    const float down = pow2(-e2);
+    // the sign of the score's factor goes into the queries, so that larger products are
+    // larger scores
+    const float down = a.scale > 0.f ? pow2(-e2) : a.scale < 0.f ? -pow2(-e2) : 0.f;
 #pragma unroll
     for (int e = 0; e < NB; ++e)
 #pragma unroll
@@ -202,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
         for (int x = 0; x < 4; ++x) h[x] = pack_f16x2(bf16_lo(raw[e][w][x]) * down, bf16_hi(raw[e][w][x]) * down);
         q[j][e][w] = __builtin_bit_cast(f16x8, h);
       }
-    factor[j] = a.scale * (kLog2e * lv.inv_kappa) * pow2(e2);
+    factor[j] = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * (kLog2e * lv.inv_kappa) * pow2(e2);
   }
   const int all_low = seen_low(a, seq, i_last), all_high = seen_high(a, seq, i_first);   // seen by every row
 
@@ -216,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
   const int tr_pos = (((lane & 7) >> 2) << 4) | (quad << 2) | (lane & 3), tr_sel = (lane >> 3) & 1;
 
   f32x4 o[kNQ][4 * NB];
-  float m[kNQ], l[kNQ];                         // m: maximum of score + exponent of the tile's value scales
+  float m[kNQ], l[kNQ];                         // m: reference, about the maximum of score + exponent of the value scales
 #pragma unroll
   for (int j = 0; j < kNQ; ++j) {
     m[j] = -INFINITY, l[j] = 0.f;
@@ -226,13 +243,11 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
 
   for (int k = 0; k < mine; ++k) {
     const int pos0 = t0 + (k * kWaves + wave) * kTile;
-    const bool whole = pos0 >= all_low && pos0 + kTile <= min(all_high, t1) && ((held >> (2 * (k & 31))) & 3) == 3;
     const uint32_t pages_ok = (uint32_t)(held >> (2 * (k & 31))) & 3u;
-    Tile<D> next;
-    if (k + 1 < mine) {
+    bool whole = pos0 >= all_low && pos0 + kTile <= min(all_high, t1) && pages_ok == 3;
+    if (k + 1 < mine) {                           // (the last tile's rows are loaded twice, into nothing)
       if (((k + 1) & 31) == 0) found = find_rows(k + 1, held);
       tile_rows(k + 1, row);
-      load_tile<D>(next, a.c, row, lane);
     }
     // value rows into LDS
 #pragma unroll
@@ -247,7 +262,8 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
               u32x4{cur.v[g][p][0], cur.v[g][p][1], cur.v[g][p][2], cur.v[g][p][3]};
         }
       }
-    // scores: x[j][g][i] of position 16 g + 4 quad + i
+    load_values<D>(cur, a.c, row, lane);
+    // scores over factor: x[j][g][i] of position 16 g + 4 quad + i
     float x[kNQ][2][4];
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
@@ -262,15 +278,33 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
           for (int i = 0; i < 4; ++i) {
             const float ks = bf16_at(cur.ks[g], i * NB + e);
             x[j][g][i] = e == 0 ? ks * s[i] : __builtin_fmaf(ks, s[i], x[j][g][i]);
-            if (e == NB - 1) x[j][g][i] *= factor[j];
           }
         }
       }
     }
-    if (!whole) {
+    load_keys<D>(cur, a.c, row, lane);
+    load_scales<D>(cur.ks, a.c.scales[0], row, lane);
+    // the exponent of the largest value scale (bf16 patterns of positive numbers order
+    // like the numbers, with infinity and NaN on top)
+    auto top_scale = [&]() -> int {
+      typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+      u16x2 vm = {0, 0};
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int w = 0; w < T::kScaleWords; ++w)
+          vm = __builtin_elementwise_max(vm, __builtin_bit_cast(u16x2, cur.vs[g][w]));
+      uint32_t v = max((uint32_t)vm[0], (uint32_t)vm[1]);
+      auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+      v = max(r[0], r[1]);
+      r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+      return (int)(__builtin_amdgcn_readfirstlane(max(r[0], r[1])) >> 7);
+    };
+    int ve = top_scale();
+    if (!whole || ve >= 255) {
       // hidden positions: score -infinity.  A value scale goes to 0 where no row sees the
-      // position (stale rows), and where it is NaN, the scores of the rows that do see it
-      // turning NaN instead: 0 x NaN in the product would reach the rows that do not.
+      // position (stale rows), and where it is not finite, the scores of the rows that do
+      // see it turning NaN instead: 0 x NaN in the product would reach the rows that do not.
 #pragma unroll
       for (int g = 0; g < 2; ++g)
 #pragma unroll
@@ -291,19 +325,9 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
             if (!(there && pos >= qlow[j] && pos < qhigh[j])) x[j][g][i] = -INFINITY;
           }
         }
+      ve = top_scale();
     }
-    // the largest value scale's exponent (bf16 patterns of positive numbers order like
-    // the numbers; + 0x40 turns NaN negative)
-    typedef short s16x2 __attribute__((ext_vector_type(2)));
-    s16x2 vm = {0, 0};
-#pragma unroll
-    for (int g = 0; g < 2; ++g)
-#pragma unroll
-      for (int w = 0; w < T::kScaleWords; ++w)
-        vm = __builtin_elementwise_max(vm, __builtin_bit_cast(s16x2, cur.vs[g][w]) + s16x2{0x40, 0x40});
-    const float vtop = rows_max(__uint_as_float((uint32_t)max((int)max(vm[0], vm[1]) - 0x40, 0) << 16));
-    const int ev = min(max((int)(__builtin_amdgcn_readfirstlane(__float_as_uint(vtop)) >> 23) - 127, kMinEv), 126);
-    const float vdown = pow2(-ev), fev = (float)ev;
+    const float fev = (float)max(ve - 127, kMinEv);
 #pragma unroll
     for (int j = 0; j < kNQ; ++j) {
       float top = -INFINITY;
@@ -311,36 +335,31 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
       for (int g = 0; g < 2; ++g)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, x[j][g][i]);
-      const float mn = fmaxf(m[j], rows_max(top) + fev);
-      const float ref = mn == -INFINITY ? 0.f : mn;
-      if (__any(mn > m[j])) {
-        const float alpha = exp2_fast(m[j] - ref);
+      const float mn = __builtin_fmaf(rows_max(top), factor[j], fev);
+      if (__any(mn > m[j] + kSlack)) {
+        const float up = fmaxf(m[j], mn);
+        const float alpha = exp2_fast(m[j] - (up == -INFINITY ? 0.f : up));
         l[j] *= alpha;
 #pragma unroll
         for (int c = 0; c < 4 * NB; ++c)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[j][c][i] *= alpha;
-        m[j] = mn;
+        m[j] = up;
       }
-      float sum = 0.f;
+      const float ref = m[j] == -INFINITY ? 0.f : m[j];
 #pragma unroll
       for (int g = 0; g < 2; ++g)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[j][g][i] = exp2_fast(x[j][g][i] + (fev - ref));
-          sum += x[j][g][i];
+          x[j][g][i] = exp2_fast(__builtin_fmaf(x[j][g][i], factor[j], -ref));
+          l[j] += x[j][g][i];
         }
-      l[j] = __builtin_fmaf(sum, vdown, l[j]);
     }
-    // weights x value scales, as the second operand of each run's products
+    // weights x value scales (at most 2^(kSlack + 1)), as the second operand of each
+    // run's products
     f16x8 pv[kNQ][NB];
 #pragma unroll
-    for (int e = 0; e < NB; ++e) {
-      float vs[2][4];
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) vs[g][i] = bf16_at(cur.vs[g], i * NB + e) * vdown;
+    for (int e = 0; e < NB; ++e)
 #pragma unroll
       for (int j = 0; j < kNQ; ++j) {
         u32x4 h;
@@ -348,11 +367,11 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
         for (int g = 0; g < 2; ++g)
 #pragma unroll
           for (int i = 0; i < 4; i += 2)
-            h[2 * g + i / 2] = pack_f16x2(x[j][g][i] * vs[g][i],
-                                          x[j][g][i + 1] * vs[g][i + 1]);
+            h[2 * g + i / 2] = pack_f16x2(x[j][g][i] * bf16_at(cur.vs[g], i * NB + e),
+                                          x[j][g][i + 1] * bf16_at(cur.vs[g], (i + 1) * NB + e));
         pv[j][e] = __builtin_bit_cast(f16x8, h);
       }
-    }
+    load_scales<D>(cur.vs, a.c.scales[1], row, lane);
 #pragma unroll
     for (int c = 0; c < 4 * NB; c += 2) {
       const i32x2 w = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
@@ -364,7 +383,6 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
         for (int j = 0; j < kNQ; ++j) o[j][c + h] = mfma16(v, pv[j][(c + h) >> 2], o[j][c + h]);
       }
     }
-    cur = next;
   }
 
   // ---- join the eight waves
@@ -434,16 +452,14 @@ int tile_rows_of(const AttnArgs& a) { return a.max_q * (a.q_heads / a.c.heads) <
 
 template <int D, int kNQ>
 hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Partial& part, hipStream_t s) {
-  const hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kv_decode_kernel<D, kNQ>), Smem<D, kNQ>::kBytes);
-  if (e != hipSuccess) return e;
   hipLaunchKernelGGL((kv_decode_kernel<D, kNQ>), dim3((unsigned)(sp.splits * sp.tiles * a.c.heads), (unsigned)a.seqs),
-                     dim3(kThreads), (Smem<D, kNQ>::kBytes), s, a, sp, lv, part);
+                     dim3(kThreads), 0, s, a, sp, lv, part);
   return hipGetLastError();
 }
 
 }  // namespace
 
-Split decode_split(const AttnArgs& a) { return split_of(a, tile_rows_of(a), 768, kRound); }
+Split decode_split(const AttnArgs& a) { return split_of(a, tile_rows_of(a), 512, kRound); }
 
 hipError_t launch_decode(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s) {
   const Levels& lv = levels_of(a.c.table);

@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 
-from ._lib import _check, _i64, _stream, lib
+from ._lib import _check, _i64, lib
 
 
 class _CacheStruct(ctypes.Structure):
@@ -76,6 +76,14 @@ def kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, device="c
     return KVCache(*t, table)
 
 
+def _raw_stream(stream, device) -> int:
+    """The hipStream_t of `stream`, or of the device's current stream.  (The raw
+    query takes 0.1 us; building a torch.cuda.Stream for it takes 3 us, as long as
+    the launch.)"""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
 def _dtype_code(dtype) -> int:
     import torch
     if dtype == torch.bfloat16:
@@ -107,7 +115,7 @@ def kv_write(k, v, cache: KVCache, slots, stream=None) -> None:
         raise ValueError("kv_write: the last axis of k and v must be contiguous")
     _check(lib().qlora_kv_write(cache._ref, k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype), n,
                                 (_i64 * 4)(ks[0], ks[1], vs[0], vs[1]), _ints(slots, "slots", (n,), device),
-                                _stream(stream)), "qlora_kv_write")
+                                _raw_stream(stream, device)), "qlora_kv_write")
 
 
 def kv_read(cache: KVCache, slots, dtype=None, stream=None):
@@ -120,7 +128,7 @@ def kv_read(cache: KVCache, slots, dtype=None, stream=None):
     k = torch.empty((n, cache.kv_heads, cache.head_dim), dtype=dtype, device=device)
     v = torch.empty_like(k)
     _check(lib().qlora_kv_read(cache._ref, _ints(slots, "slots", (n,), device), n, _dtype_code(dtype), k.data_ptr(),
-                               v.data_ptr(), _stream(stream)), "qlora_kv_read")
+                               v.data_ptr(), _raw_stream(stream, device)), "qlora_kv_read")
     if stream is not None:   # allocated on the current stream, written on another
         k.record_stream(stream)
         v.record_stream(stream)
@@ -173,7 +181,7 @@ def kv_attention(q, cache: KVCache, block_table, lengths, q_starts=None, max_q=N
         _ints(block_table, "block_table", (seqs, width), device), width, _ints(lengths, "lengths", (seqs,), device),
         None if q_starts is None else _ints(q_starts, "q_starts", (seqs + 1,), device), seqs, max_q, max_len,
         dim ** -0.5 if scale is None else scale, causal, window, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream)),
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, device)),
         "qlora_kv_attention")
     if stream is not None:   # allocated on the current stream, used on another
         for t in (out, lse, workspace):
