@@ -12,14 +12,19 @@ namespace qlora {
 namespace kv {
 namespace {
 
-// Joins the splits of one row a wave.
+// Joins the splits of one row a workgroup: D / 4 lanes hold four elements each,
+// and 1024 / D groups of them take the splits in turn.
+constexpr int kMaxSplits = 128;
+
 template <int D>
 __global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a, Split sp, float inv_kappa, Partial part) {
-  constexpr int E = D / 64;
-  const int lane = threadIdx.x & 63;
+  constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
+  __shared__ float weight[kMaxSplits];
+  __shared__ float2 total;
+  __shared__ f32x4 acc[256];
+  const int tid = threadIdx.x, lane = tid & 63;
   const int group = (int)a.q_heads / (int)a.c.heads;
-  const int per = (sp.rows + 3) / 4;             // workgroups of four waves a head
-  const int r = blockIdx.x % per * 4 + (threadIdx.x >> 6), head = blockIdx.x / per, b = blockIdx.y;
+  const int r = blockIdx.x % sp.rows, head = blockIdx.x / sp.rows, b = blockIdx.y;
   const Seq seq = sequence(a, b);
   const int rows = seq.n * group;
   if (r >= rows) return;
@@ -28,43 +33,47 @@ __global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a, Split sp, floa
   const int live = live_splits(span, sp.chunk, sp.splits);
   const int i = r / group;
   const int64_t row = (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
-  const float2* stat = part.stat + row * sp.splits;
-  const float* o = part.o + row * sp.splits * D + lane * E;
-  float top = -INFINITY;
-  for (int s = lane; s < live; s += 64) top = fmaxf(top, stat[s].x);
+  const int g = tid / kLanes, at = tid % kLanes;
+  const f32x4* o = reinterpret_cast<const f32x4*>(part.o + row * sp.splits * D) + at;
+  if (tid < 64) {
+    float2 st[kMaxSplits / 64];
+    float top = -INFINITY, sum = 0.f;
 #pragma unroll
-  for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-  const float ref = top == -INFINITY ? 0.f : top;
-  float sum = 0.f, acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int s0 = 0; s0 < live; s0 += 64) {
-    float f = 0.f;
-    if (s0 + lane < live) {
-      const float2 st = stat[s0 + lane];
-      f = exp2_fast(st.x - ref);
-      sum = __builtin_fmaf(f, st.y, sum);
+    for (int h = 0; h < kMaxSplits / 64; ++h) {
+      const int s = 64 * h + lane;
+      st[h] = s < live ? part.stat[row * sp.splits + s] : make_float2(-INFINITY, 0.f);
+      top = fmaxf(top, st[h].x);
     }
-    const int cnt = min(64, live - s0);
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+    const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int h = 0; h < kMaxSplits / 64; ++h) {
+      const float f = exp2_fast(st[h].x - ref);
+      weight[64 * h + lane] = f;
+      sum = __builtin_fmaf(f, st[h].y, sum);
+    }
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
+    if (lane == 0) total = make_float2(top, sum);
+  }
+  __syncthreads();
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int s = 0; s < cnt; ++s) {
-      const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s));
-      const float* src = o + (int64_t)(s0 + s) * D;
+  for (int s = g; s < live; s += kGroups) {
+    const float f = weight[s];
+    const f32x4 p = o[(int64_t)s * (D / 4)];
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(fs, src[e], acc[e]);
-    }
+    for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, p[e], v[e]);
   }
+  acc[tid] = v;
+  __syncthreads();
+  if (tid >= kLanes) return;
 #pragma unroll
-  for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
-  const float inv = sum == 0.f ? 0.f : inv_kappa / sum;
-  uint16_t* out = a.out + row * D + lane * E;
-  if constexpr (E == 1) {
-    *out = (uint16_t)pack_bf16x2(acc[0] * inv, 0.f);
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; e += 2) reinterpret_cast<uint32_t*>(out)[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  }
-  if (a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : kLn2 * (top + __builtin_amdgcn_logf(sum));
+  for (int h = 1; h < kGroups; ++h) v += acc[h * kLanes + tid];
+  const float top = total.x, sum = total.y, inv = sum == 0.f ? 0.f : inv_kappa / sum;
+  reinterpret_cast<u32x2*>(a.out + row * D)[tid] = u32x2{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
+  if (a.lse && tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : kLn2 * (top + __builtin_amdgcn_logf(sum));
 }
 
 // fp32 -> fp16 bits, round to nearest even, for magnitudes of fp16's normal range (or 0).
@@ -94,8 +103,7 @@ const Levels& levels_of(int table) {
   return lv[table];
 }
 
-Split split_of(const AttnArgs& a, int tile_rows, int fill, int least) {
-  constexpr int kMaxSplits = 128;
+Split split_of(const AttnArgs& a, int tile_rows, int fill, int least, int alone) {
   Split s;
   s.rows = (int)(a.max_q * (a.q_heads / a.c.heads));
   s.tile_rows = tile_rows;
@@ -105,8 +113,8 @@ Split split_of(const AttnArgs& a, int tile_rows, int fill, int least) {
   span = std::max<int64_t>(span, 1);
   const int64_t groups = a.seqs * a.c.heads * s.tiles;
   const int64_t splits = std::min<int64_t>(std::max<int64_t>(1, fill / groups), kMaxSplits);
-  const int64_t each = std::max<int64_t>(least, (span + splits - 1) / splits);
-  s.chunk = (int)((each + least - 1) / least * least);
+  const int64_t each = span <= alone ? span : std::max<int64_t>(least, (span + splits - 1) / splits);
+  s.chunk = (int)((each + 255) / 256 * 256);
   s.splits = (int)((span + s.chunk - 1) / s.chunk);
   return s;
 }
@@ -131,7 +139,7 @@ hipError_t launch_kv_attention(const AttnArgs& a, hipStream_t s) {
   part.stat = reinterpret_cast<float2*>(part.o + (size_t)(a.tokens * a.q_heads) * sp.splits * a.c.D);
   const hipError_t e = few_rows(a) ? launch_decode(a, sp, part, s) : launch_prompt(a, sp, part, s);
   if (e != hipSuccess || sp.splits == 1) return e;
-  const dim3 grid((unsigned)((sp.rows + 3) / 4 * a.c.heads), (unsigned)a.seqs);
+  const dim3 grid((unsigned)(sp.rows * a.c.heads), (unsigned)a.seqs);
   const auto kernel = a.c.D == 64 ? kv_join_kernel<64> : a.c.D == 128 ? kv_join_kernel<128> : kv_join_kernel<256>;
   hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, sp, levels_of(a.c.table).inv_kappa, part);
   return hipGetLastError();

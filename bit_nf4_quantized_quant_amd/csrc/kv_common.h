@@ -37,8 +37,8 @@ struct Partial {
 };
 
 // Splits such that about `fill` workgroups share the work, of at least
-// `least` positions each (and a multiple of that).
-Split split_of(const AttnArgs& a, int tile_rows, int fill, int least);
+// `least` positions each; up to `alone` positions are not split.
+Split split_of(const AttnArgs& a, int tile_rows, int fill, int least, int alone);
 
 // Attention for few query rows (kv_decode.hip) and for many (kv_prompt.hip).
 Split decode_split(const AttnArgs& a);

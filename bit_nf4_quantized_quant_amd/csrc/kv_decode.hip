@@ -129,7 +129,7 @@ struct Smem {
 };
 
 template <int D, int kNQ>
-__global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
+__global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 4 : 2)
     kv_decode_kernel(AttnArgs a, Split sp, Levels lv, Partial part) {
   using T = Tile<D>;
   constexpr int NB = D / 64, kRows = 16 * kNQ;
@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
   const int split = blockIdx.x % sp.splits, b = blockIdx.y;
   const int head = blockIdx.x / sp.splits / sp.tiles, r0 = blockIdx.x / sp.splits % sp.tiles * kRows;
   const int group = (int)a.q_heads / (int)a.c.heads;
+  build_pairs<kThreads>(lv, lut);               // (while the sequence's numbers are on their way)
   const Seq seq = sequence(a, b);
   const int rows = seq.n * group;
   if (r0 >= rows) return;
@@ -223,8 +224,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256 || kNQ > 1) ? 2 : 4)
   }
   const int all_low = seen_low(a, seq, i_last), all_high = seen_high(a, seq, i_first);   // seen by every row
 
-  build_pairs<kThreads>(lv, lut);
-  __syncthreads();
+  __syncthreads();                              // (the pair table)
 
   const uint32_t lane4 = 4u * (lane & 31);
   char* vbuf = lut + wave * (16 * 256);         // 16 pieces of 128 bytes (32 for D = 256, 8 for D = 64)
@@ -459,7 +459,7 @@ hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Pa
 
 }  // namespace
 
-Split decode_split(const AttnArgs& a) { return split_of(a, tile_rows_of(a), 512, kRound); }
+Split decode_split(const AttnArgs& a) { return split_of(a, tile_rows_of(a), 512, 512, 1280); }
 
 hipError_t launch_decode(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s) {
   const Levels& lv = levels_of(a.c.table);

@@ -370,7 +370,7 @@ hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Pa
 }  // namespace
 
 // One workgroup fills a CU: the positions are split where there are fewer.
-Split prompt_split(const AttnArgs& a) { return split_of(a, kRows, 256, 512); }
+Split prompt_split(const AttnArgs& a) { return split_of(a, kRows, 256, 512, 1024); }
 
 hipError_t launch_prompt(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s) {
   const Levels& lv = levels_of(a.c.table);

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 
 from ._lib import _check, _i64, lib
 
@@ -135,12 +136,20 @@ def kv_read(cache: KVCache, slots, dtype=None, stream=None):
     return k, v
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(kv_heads, page_size, head_dim, q_heads, tokens, seqs, max_q, max_len, window) -> int:
+    """qlora_kv_attention_workspace: a function of these sizes alone."""
+    c = _CacheStruct(None, None, None, None, 1, kv_heads, page_size, head_dim, 0)
+    return lib().qlora_kv_attention_workspace(ctypes.byref(c), q_heads, tokens, seqs, max_q, max_len, window)
+
+
 def kv_attention_workspace(cache: KVCache, q_heads: int, tokens: int, seqs: int, max_q: int, max_len: int,
                            window: int = 0):
-    """A workspace for kv_attention calls of at most these sizes (any content)."""
+    """A workspace for kv_attention calls of these sizes (any content), or None
+    where they need none."""
     import torch
-    n = lib().qlora_kv_attention_workspace(cache._ref, q_heads, tokens, seqs, max_q, max_len, window)
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=cache.k_codes.device)
+    n = _workspace_bytes(cache.kv_heads, cache.page_size, cache.head_dim, q_heads, tokens, seqs, max_q, max_len, window)
+    return torch.empty(n, dtype=torch.uint8, device=cache.k_codes.device) if n else None
 
 
 def kv_attention(q, cache: KVCache, block_table, lengths, q_starts=None, max_q=None, max_len=None, scale=None,
@@ -181,7 +190,8 @@ def kv_attention(q, cache: KVCache, block_table, lengths, q_starts=None, max_q=N
         _ints(block_table, "block_table", (seqs, width), device), width, _ints(lengths, "lengths", (seqs,), device),
         None if q_starts is None else _ints(q_starts, "q_starts", (seqs + 1,), device), seqs, max_q, max_len,
         dim ** -0.5 if scale is None else scale, causal, window, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, device)),
+        None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel(), _raw_stream(stream, device)),
         "qlora_kv_attention")
     if stream is not None:   # allocated on the current stream, used on another
         for t in (out, lse, workspace):
