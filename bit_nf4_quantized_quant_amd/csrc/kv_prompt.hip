@@ -20,7 +20,6 @@
 #include <algorithm>
 
 #include "kv_common.h"
-#include "launch.h"
 
 namespace qlora {
 namespace kv {
@@ -49,16 +48,11 @@ struct Shape {
   static constexpr size_t kBytes = kScaleOff + kWaves * 512;
 };
 
-// Where one lane finds its share of a tile.
-struct Rows {
-  uint32_t code, scale;   // cache rows of the position whose codes, and whose scales, it loads
-  bool ok;                // the scales' positions are there (two of them for D = 64: bit 0 and bit 1)
-  bool ok2;
-};
+// One lane's share of a tile on its way.
 struct Raw {
   u32x2 k, v;             // 16 codes each
   uint32_t ks, vs;        // two scales each
-  bool ok, ok2;
+  uint32_t keep;          // the halves of ks and vs whose positions are there
 };
 
 __device__ __forceinline__ float half_max(float v) {   // over a wave's two halves
@@ -69,20 +63,31 @@ __device__ __forceinline__ float half_add(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
-// The largest of the wave's finite bf16 numbers (two a lane), as its exponent.
-__device__ __forceinline__ int top_exponent(uint32_t pair) {
-  typedef short s16x2 __attribute__((ext_vector_type(2)));
-  const s16x2 p = __builtin_bit_cast(s16x2, pair) + s16x2{0x40, 0x40};   // NaN turns negative
-  int v = max((int)max(p[0], p[1]), 0x40);
-  v = max(v, __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, false));
-  v = max(v, __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, false));
-  v = max(v, __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, false));
-  v = max(v, __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, false));
-  auto r = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
-  v = max((int)r[0], (int)r[1]);
-  r = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
-  v = __builtin_amdgcn_readfirstlane(max((int)r[0], (int)r[1])) - 0x40;
-  return min(max((v >> 7) - 127, kMinExp), 126);
+// The exponents of the wave's largest finite bf16 numbers, two a lane in k and in v
+// (patterns of positive numbers order like the numbers; + 0x40 turns NaN negative).
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+template <int ctrl>
+__device__ __forceinline__ s16x2 max_dpp(s16x2 v) {
+  return __builtin_elementwise_max(
+      v, __builtin_bit_cast(s16x2, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), ctrl, 0xF, 0xF, false)));
+}
+__device__ __forceinline__ void top_exponents(uint32_t k, uint32_t v, int& ek, int& ev) {
+  // low halves: keys, high halves: values
+  s16x2 t = __builtin_elementwise_max(__builtin_bit_cast(s16x2, __builtin_amdgcn_perm(v, k, 0x05040100u)) + s16x2{0x40, 0x40},
+                                      __builtin_bit_cast(s16x2, __builtin_amdgcn_perm(v, k, 0x07060302u)) + s16x2{0x40, 0x40});
+  t = max_dpp<0xB1>(t);
+  t = max_dpp<0x4E>(t);
+  t = max_dpp<0x141>(t);
+  t = max_dpp<0x140>(t);
+  const uint32_t u = __builtin_bit_cast(uint32_t, t);
+  auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  t = __builtin_elementwise_max(__builtin_bit_cast(s16x2, r[0]), __builtin_bit_cast(s16x2, r[1]));
+  const uint32_t x = __builtin_bit_cast(uint32_t, t);
+  r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  t = __builtin_elementwise_max(__builtin_bit_cast(s16x2, r[0]), __builtin_bit_cast(s16x2, r[1]));
+  const uint32_t y = (uint32_t)__builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, t));
+  ek = min(max((max((int)(int16_t)y, 0x40) - 0x40 >> 7) - 127, kMinExp), 126);
+  ev = min(max((max((int)(int16_t)(y >> 16), 0x40) - 0x40 >> 7) - 127, kMinExp), 126);
 }
 
 template <int D>
@@ -90,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     kv_prompt_kernel(AttnArgs a, Split sp, Levels lv, Partial part) {
   using S = Shape<D>;
   constexpr int NB = S::NB, NP = S::NP, NU = S::NU, NS = S::NS, kTile = S::kTile;
-  extern __shared__ __attribute__((aligned(256))) char smem[];
+  __shared__ __attribute__((aligned(256))) char smem[S::kBytes];
   char* lut = smem;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
@@ -150,35 +155,30 @@ __global__ void __launch_bounds__(kThreads, 2)
   // ---- a tile's way into LDS
   const int32_t* table = a.block_table + (int64_t)b * a.table_width;
   const int wp = wave / NU, wu = wave % NU;     // this wave's part of the positions and of the elements
-  auto row_of = [&](int t, bool& ok) -> uint32_t {
-    ok = t < t1;
-    uint32_t row = 0;
-    if (ok) {
-      const uint32_t pg = div_by((uint32_t)t, a.c.page_div);
-      const uint32_t page = (uint32_t)table[pg];
-      ok = page < a.c.pages;
-      if (ok) row = (page * a.c.heads + head) * a.c.page_size + ((uint32_t)t - pg * a.c.page_size);
-    }
-    return row;
+  // The scales of a tile are its first positions' first: lane l loads numbers 2 l and
+  // 2 l + 1 of [position][run], whose position is spos, and takes the row of the position
+  // whose codes it loads, 32 wp + col, from the lane that has it.
+  const int spos = D == 64 ? 2 * lane : D == 128 ? lane : lane >> 1;
+  const int from = (D == 64 ? (32 * wp + col) >> 1 : D == 128 ? 32 * wp + col : 2 * (32 * wp + col)) * 4;
+  const int last = (int)a.table_width - 1;
+  auto find_page = [&](int k) -> uint32_t {     // (issued a tile before its use)
+    return (uint32_t)table[min((int)div_by((uint32_t)(t0 + k * kTile + spos), a.c.page_div), last)];
   };
-  auto find = [&](int k) -> Rows {
-    Rows f;
-    bool unused;
-    f.code = row_of(t0 + k * kTile + 32 * wp + col, unused);
-    const int st = t0 + k * kTile + (D == 64 ? 2 * lane : D == 128 ? lane : lane >> 1);
-    f.scale = row_of(st, f.ok);
-    f.ok2 = D == 64 ? f.ok && st + 1 < t1 : f.ok;
-    return f;
-  };
-  auto load = [&](const Rows& f) -> Raw {
+  auto load = [&](int k, uint32_t page) -> Raw {
     Raw w;
-    const uint64_t at = (uint64_t)f.code * (D / 2) + (uint32_t)(wu * 16 + half * 8);
+    const int t = t0 + k * kTile + spos;
+    const bool ok = t < t1 && page < a.c.pages;
+    const uint32_t row =
+        ok ? (page * a.c.heads + head) * a.c.page_size + ((uint32_t)t - div_by((uint32_t)t, a.c.page_div) * a.c.page_size) : 0;
+    uint32_t code_row = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)row);
+    if (D == 64) code_row += col & 1;
+    const uint64_t at = (uint64_t)code_row * (D / 2) + (uint32_t)(wu * 16 + half * 8);
     w.k = *reinterpret_cast<const u32x2*>(a.c.codes[0] + at);
     w.v = *reinterpret_cast<const u32x2*>(a.c.codes[1] + at);
-    const uint64_t sat = (uint64_t)f.scale * NB + (D == 256 ? 2 * (lane & 1) : 0);
+    const uint64_t sat = (uint64_t)row * NB + (D == 256 ? 2 * (lane & 1) : 0);
     w.ks = *reinterpret_cast<const uint32_t*>(a.c.scales[0] + sat);
     w.vs = *reinterpret_cast<const uint32_t*>(a.c.scales[1] + sat);
-    w.ok = f.ok, w.ok2 = f.ok2;
+    w.keep = !ok ? 0u : D == 64 && t + 1 >= t1 ? 0xFFFFu : 0xFFFFFFFFu;
     return w;
   };
   const uint32_t lane4 = 4u * (lane & 31);
@@ -193,11 +193,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
   auto stage = [&](Raw w, int buf) -> Meta {
     Meta meta;
-    meta.full = __all(w.ok && w.ok2);
-    const uint32_t keep = (w.ok ? 0xFFFFu : 0u) | (w.ok2 ? 0xFFFF0000u : 0u);
-    w.ks &= keep, w.vs &= keep;
-    meta.ek = top_exponent(w.ks);
-    meta.ev = top_exponent(w.vs);
+    meta.full = __all(w.keep == 0xFFFFFFFFu);
+    w.ks &= w.keep, w.vs &= w.keep;
+    top_exponents(w.ks, w.vs, meta.ek, meta.ev);
     const float kd = pow2(-meta.ek), vd = pow2(-meta.ev);
     float k0 = bf16_lo(w.ks) * kd, k1 = bf16_hi(w.ks) * kd, v0 = bf16_lo(w.vs) * vd, v1 = bf16_hi(w.vs) * vd;
     // a value scale that is not finite turns its position's scores NaN instead of the
@@ -236,16 +234,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     return meta;
   };
 
-  build_pairs<kThreads>(lv, lut);
-  Rows found = find(0);
-  Raw raw = load(found);
-  found = find(1);
-  __syncthreads();
   Meta meta{0, 0, false};
-  if (tiles > 0) meta = stage(raw, 0);
-  raw = load(found);
-  found = find(2);
-  __syncthreads();
+  Raw raw;
+  uint32_t page = 0;
+  if (tiles > 0) {                              // (a table without entries has no tiles)
+    const uint32_t p0 = find_page(0), p1 = find_page(1);
+    page = find_page(2);
+    const Raw first = load(0, p0);
+    raw = load(1, p1);
+    build_pairs<kThreads>(lv, lut);
+    __syncthreads();
+    meta = stage(first, 0);
+    __syncthreads();
+  }
 
   f32x16 o[NU];
 #pragma unroll
@@ -255,8 +256,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   float m = -INFINITY, l = 0.f;                 // m: reference of score + exponent of the tile's value scales
 
   for (int k = 0; k < tiles; ++k) {
-    const Raw next = load(found);
-    found = find(k + 3);
+    const uint32_t page_now = page;
+    page = find_page(k + 3);
+    const Raw next = load(k + 2, page_now);
     const int pos0 = t0 + k * kTile;
     const Meta now = meta;
     if (pos0 < any_high && pos0 + kTile > any_low) {
@@ -267,19 +269,26 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int p = 0; p < NP; ++p)
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[p][i] = 0.f;
+      // operands are read kAhead products before their use
+      constexpr int kAhead = 4;
+      f16x8 kf[kAhead];
+      auto key = [&](int y) { return *reinterpret_cast<const f16x8*>(kbuf + ((y % NP * NS + y / NP) * 64 + lane) * 16); };
 #pragma unroll
-      for (int x = 0; x < NS; ++x)
+      for (int y = 0; y < kAhead; ++y) kf[y] = key(y);
 #pragma unroll
-        for (int p = 0; p < NP; ++p)
-          s[p] = mfma32(*reinterpret_cast<const f16x8*>(kbuf + ((p * NS + x) * 64 + lane) * 16), q[x], s[p]);
+      for (int y = 0; y < NP * NS; ++y) {
+        const f16x8 now_k = kf[y % kAhead];
+        if (y + kAhead < NP * NS) kf[y % kAhead] = key(y + kAhead);
+        s[y % NP] = mfma32(now_k, q[y / NP], s[y % NP]);
+      }
       if (!(now.full && pos0 >= all_low && pos0 + kTile <= all_high)) {
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           uint32_t ok = 0xFFFFFFFFu;
-          if (!now.full) {                      // which positions are there: 16 share a page
-            bool here;
-            row_of(pos0 + 32 * p + col, here);
-            ok = (uint32_t)__ballot(here);
+          if (!now.full) {                      // which positions are there
+            const int t = pos0 + 32 * p + col;
+            const uint32_t pg = (uint32_t)table[min((int)div_by((uint32_t)t, a.c.page_div), last)];
+            ok = (uint32_t)__ballot(t < t1 && pg < a.c.pages);
           }
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -360,10 +369,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 template <int D>
 hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Partial& part, hipStream_t s) {
-  const hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kv_prompt_kernel<D>), Shape<D>::kBytes);
-  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kv_prompt_kernel<D>, dim3((unsigned)(sp.splits * sp.tiles * a.c.heads), (unsigned)a.seqs),
-                     dim3(kThreads), Shape<D>::kBytes, s, a, sp, lv, part);
+                     dim3(kThreads), 0, s, a, sp, lv, part);
   return hipGetLastError();
 }
 
