@@ -44,15 +44,11 @@ struct Shape {
   static constexpr int NS = D / 16;             // reduction steps of a score
   static constexpr int kOperand = 16384;        // bytes of a tile's fp16 keys, or values
   static constexpr int kRawOff = kPairBytes + 4 * kOperand;
+  // sixteen tiles' scales: fp16 [position][run] of the keys, [run][position] of the
+  // values, and the tile's exponents
   static constexpr int kScaleOff = kRawOff + kWaves * 512;
-  static constexpr size_t kBytes = kScaleOff + kWaves * 512;
-};
-
-// One lane's share of a tile on its way.
-struct Raw {
-  u32x2 k, v;             // 16 codes each
-  uint32_t ks, vs;        // two scales each
-  uint32_t keep;          // the halves of ks and vs whose positions are there
+  static constexpr int kScaleSize = 256 + 256 + 16;
+  static constexpr size_t kBytes = kScaleOff + 16 * kScaleSize;
 };
 
 __device__ __forceinline__ float half_max(float v) {   // over a wave's two halves
@@ -71,6 +67,14 @@ __device__ __forceinline__ s16x2 max_dpp(s16x2 v) {
   return __builtin_elementwise_max(
       v, __builtin_bit_cast(s16x2, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), ctrl, 0xF, 0xF, false)));
 }
+template <int lanes>
+__device__ __forceinline__ s16x2 max_swapped(s16x2 v) {   // between rows of 16 lanes, or halves of 32
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto r = lanes == 16 ? __builtin_amdgcn_permlane16_swap(u, u, false, false)
+                             : __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t r0 = r[0], r1 = r[1];   // (copies: a bit cast of an element takes element 0 whatever the index)
+  return __builtin_elementwise_max(__builtin_bit_cast(s16x2, r0), __builtin_bit_cast(s16x2, r1));
+}
 __device__ __forceinline__ void top_exponents(uint32_t k, uint32_t v, int& ek, int& ev) {
   // low halves: keys, high halves: values
   s16x2 t = __builtin_elementwise_max(__builtin_bit_cast(s16x2, __builtin_amdgcn_perm(v, k, 0x05040100u)) + s16x2{0x40, 0x40},
@@ -79,15 +83,11 @@ __device__ __forceinline__ void top_exponents(uint32_t k, uint32_t v, int& ek, i
   t = max_dpp<0x4E>(t);
   t = max_dpp<0x141>(t);
   t = max_dpp<0x140>(t);
-  const uint32_t u = __builtin_bit_cast(uint32_t, t);
-  auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  t = __builtin_elementwise_max(__builtin_bit_cast(s16x2, r[0]), __builtin_bit_cast(s16x2, r[1]));
-  const uint32_t x = __builtin_bit_cast(uint32_t, t);
-  r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-  t = __builtin_elementwise_max(__builtin_bit_cast(s16x2, r[0]), __builtin_bit_cast(s16x2, r[1]));
+  t = max_swapped<16>(t);
+  t = max_swapped<32>(t);
   const uint32_t y = (uint32_t)__builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, t));
-  ek = min(max((max((int)(int16_t)y, 0x40) - 0x40 >> 7) - 127, kMinExp), 126);
-  ev = min(max((max((int)(int16_t)(y >> 16), 0x40) - 0x40 >> 7) - 127, kMinExp), 126);
+  ek = min(max(((max((int)(int16_t)y, 0x40) - 0x40) >> 7) - 127, kMinExp), 126);
+  ev = min(max(((max((int)(int16_t)(y >> 16), 0x40) - 0x40) >> 7) - 127, kMinExp), 126);
 }
 
 template <int D>
@@ -155,49 +155,53 @@ __global__ void __launch_bounds__(kThreads, 2)
   // ---- a tile's way into LDS
   const int32_t* table = a.block_table + (int64_t)b * a.table_width;
   const int wp = wave / NU, wu = wave % NU;     // this wave's part of the positions and of the elements
-  // The scales of a tile are its first positions' first: lane l loads numbers 2 l and
-  // 2 l + 1 of [position][run], whose position is spos, and takes the row of the position
-  // whose codes it loads, 32 wp + col, from the lane that has it.
-  const int spos = D == 64 ? 2 * lane : D == 128 ? lane : lane >> 1;
-  const int from = (D == 64 ? (32 * wp + col) >> 1 : D == 128 ? 32 * wp + col : 2 * (32 * wp + col)) * 4;
+  // Codes.  Lane l holds the cache row of the l-th of the 64 groups of 16 positions that
+  // the next kKnown tiles are made of (row 0 where there is none: its scales count as
+  // zero); the page numbers of the groups after them are fetched ahead.
+  constexpr int kGroups = kTile / 16, kKnown = 64 / kGroups;
   const int last = (int)a.table_width - 1;
-  auto find_page = [&](int k) -> uint32_t {     // (issued a tile before its use)
-    return (uint32_t)table[min((int)div_by((uint32_t)(t0 + k * kTile + spos), a.c.page_div), last)];
+  auto page_at = [&](int t) { return (uint32_t)table[min((int)div_by((uint32_t)t, a.c.page_div), last)]; };
+  auto row_at = [&](int t, uint32_t page, bool& ok) -> uint32_t {
+    ok = t < t1 && page < a.c.pages;
+    const uint32_t off = (uint32_t)t - div_by((uint32_t)t, a.c.page_div) * a.c.page_size;
+    return ok ? (page * a.c.heads + head) * a.c.page_size + off : 0u;
   };
-  auto load = [&](int k, uint32_t page) -> Raw {
-    Raw w;
-    const int t = t0 + k * kTile + spos;
-    const bool ok = t < t1 && page < a.c.pages;
-    const uint32_t row =
-        ok ? (page * a.c.heads + head) * a.c.page_size + ((uint32_t)t - div_by((uint32_t)t, a.c.page_div) * a.c.page_size) : 0;
-    uint32_t code_row = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)row);
-    if (D == 64) code_row += col & 1;
-    const uint64_t at = (uint64_t)code_row * (D / 2) + (uint32_t)(wu * 16 + half * 8);
-    w.k = *reinterpret_cast<const u32x2*>(a.c.codes[0] + at);
-    w.v = *reinterpret_cast<const u32x2*>(a.c.codes[1] + at);
-    const uint64_t sat = (uint64_t)row * NB + (D == 256 ? 2 * (lane & 1) : 0);
-    w.ks = *reinterpret_cast<const uint32_t*>(a.c.scales[0] + sat);
-    w.vs = *reinterpret_cast<const uint32_t*>(a.c.scales[1] + sat);
-    w.keep = !ok ? 0u : D == 64 && t + 1 >= t1 ? 0xFFFFu : 0xFFFFFFFFu;
-    return w;
+  uint32_t found = 0, ahead = 0;
+  const int cpos = 32 * wp + col;               // its codes are those of position cpos, elements 32 wu + 16 half ..
+  const char* code_base = reinterpret_cast<const char*>(a.c.codes[0]) + (cpos & 15) * (D / 2) + wu * 16 + half * 8;
+  const int64_t code_v = a.c.codes[1] - a.c.codes[0];
+  u32x2 k_raw, v_raw;
+  auto load_codes = [&](int k) {
+    const uint32_t row = (uint32_t)__shfl((int)found, k % kKnown * kGroups + (cpos >> 4));
+    const char* c = code_base + (uint64_t)row * (D / 2);
+    k_raw = *reinterpret_cast<const u32x2*>(c);
+    v_raw = *reinterpret_cast<const u32x2*>(c + code_v);
   };
-  const uint32_t lane4 = 4u * (lane & 31);
-  char* raw_v = smem + S::kRawOff + wave * 512;
-  // [position][run] of the keys, then [run][position] of the values, fp16
-  _Float16* ks_tab = reinterpret_cast<_Float16*>(smem + S::kScaleOff + wave * 512);
-  _Float16* vs_tab = ks_tab + 128;
-  // a tile's exponents and whether all of its positions are there, the same in every wave
-  struct Meta {
+  // Scales.  Every eight tiles each wave prepares the scales of one of the next eight:
+  // lane l those numbered 2 l and 2 l + 1 in the order [position][run], of position spos.
+  const int spos = D == 64 ? 2 * lane : D == 128 ? lane : lane >> 1;
+  uint32_t scale_page = 0, ks_raw = 0, vs_raw = 0, keep = 0;
+  auto scale_tile = [&](int k) { return (k & ~7) + wave; };
+  auto scales_find = [&](int k) { scale_page = page_at(t0 + scale_tile(k) * kTile + spos); };
+  auto scales_load = [&](int k) {
+    const int t = t0 + scale_tile(k) * kTile + spos;
+    bool ok;
+    const uint64_t at = (uint64_t)row_at(t, scale_page, ok) * NB + (D == 256 ? 2 * (lane & 1) : 0);
+    ks_raw = *reinterpret_cast<const uint32_t*>(a.c.scales[0] + at);
+    vs_raw = *reinterpret_cast<const uint32_t*>(a.c.scales[1] + at);
+    keep = !ok ? 0u : D == 64 && t + 1 >= t1 ? 0xFFFFu : 0xFFFFFFFFu;
+  };
+  auto scales_of = [&](int k) { return smem + S::kScaleOff + (k & 15) * S::kScaleSize; };
+  auto scales_store = [&](int k) {
+    char* dst = scales_of(scale_tile(k));
+    _Float16* ks_tab = reinterpret_cast<_Float16*>(dst);
+    _Float16* vs_tab = ks_tab + 128;
+    const int full = __all(keep == 0xFFFFFFFFu);
+    const uint32_t kw = ks_raw & keep, vw = vs_raw & keep;
     int ek, ev;
-    bool full;
-  };
-  auto stage = [&](Raw w, int buf) -> Meta {
-    Meta meta;
-    meta.full = __all(w.keep == 0xFFFFFFFFu);
-    w.ks &= w.keep, w.vs &= w.keep;
-    top_exponents(w.ks, w.vs, meta.ek, meta.ev);
-    const float kd = pow2(-meta.ek), vd = pow2(-meta.ev);
-    float k0 = bf16_lo(w.ks) * kd, k1 = bf16_hi(w.ks) * kd, v0 = bf16_lo(w.vs) * vd, v1 = bf16_hi(w.vs) * vd;
+    top_exponents(kw, vw, ek, ev);
+    const float kd = pow2(-ek), vd = pow2(-ev);
+    float k0 = bf16_lo(kw) * kd, k1 = bf16_hi(kw) * kd, v0 = bf16_lo(vw) * vd, v1 = bf16_hi(vw) * vd;
     // a value scale that is not finite turns its position's scores NaN instead of the
     // value: 0 x NaN in the product would reach the rows that do not see the position
     const bool bad0 = !(fabsf(v0) < INFINITY), bad1 = !(fabsf(v1) < INFINITY);
@@ -207,44 +211,70 @@ __global__ void __launch_bounds__(kThreads, 2)
     if constexpr (D == 64) {
       *reinterpret_cast<f16x2*>(vs_tab + 2 * lane) = f16x2{(_Float16)v0, (_Float16)v1};
     } else {
-      const int pos = D == 128 ? lane : lane >> 1, run = D == 128 ? 0 : 2 * (lane & 1);
-      vs_tab[run * kTile + pos] = (_Float16)v0;
-      vs_tab[(run + 1) * kTile + pos] = (_Float16)v1;
+      const int run = D == 128 ? 0 : 2 * (lane & 1);
+      vs_tab[run * kTile + spos] = (_Float16)v0;
+      vs_tab[(run + 1) * kTile + spos] = (_Float16)v1;
     }
-    *reinterpret_cast<u32x2*>(raw_v + lane * 8) = w.v;      // [chunk][position] of 16 codes each
-    char* kbuf = smem + kPairBytes + buf * (2 * S::kOperand);
-    char* vbuf = kbuf + S::kOperand;
-    const _Float16 ks = ks_tab[(32 * wp + col) * NB + (wu >> 1)];
-    const f16x8 ks8 = {ks, ks, ks, ks, ks, ks, ks, ks};
+    if (lane == 0) *reinterpret_cast<i32x4*>(dst + 512) = i32x4{ek, ev, full, 0};
+  };
+  const uint32_t lane4 = 4u * (lane & 31);
+  char* raw_v = smem + S::kRawOff + wave * 512;
+  // The way of a tile's share into LDS, in three steps that the products of the tile
+  // before it are put between, so that none waits for the LDS round trip of the one before.
+  f16x8 kx[2], vx[2], ks8, vs8[2];
+  i32x2 vt;
+  auto stage_fetch = [&](int k) {
+    *reinterpret_cast<u32x2*>(raw_v + lane * 8) = v_raw;    // [chunk][position] of 16 codes each
+    const _Float16 ks = reinterpret_cast<const _Float16*>(scales_of(k))[cpos * NB + (wu >> 1)];
+    ks8 = f16x8{ks, ks, ks, ks, ks, ks, ks, ks};
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-      *reinterpret_cast<f16x8*>(kbuf + ((wp * NS + 2 * wu + x) * 64 + lane) * 16) = expand8(lut, w.k[x], lane4) * ks8;
+    for (int x = 0; x < 2; ++x) kx[x] = expand8(lut, k_raw[x], lane4);
     // values: 16 lanes fetch 16 positions of their 16 elements, in the order of the scores
     const int tr_pos = ((lane >> 3) & 1) * 16 + ((lane >> 2) & 1) * 8 + half * 4 + (lane & 3);
-    const i32x2 t = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+    vt = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
         (__attribute__((address_space(3))) i32x2*)(raw_v + (((lane >> 4) & 1) * 32 + tr_pos) * 8));
+  };
+  auto stage_keys = [&](int k) {
+    char* kbuf = smem + kPairBytes + (k & 1) * (2 * S::kOperand);
+    const _Float16* vs_tab = reinterpret_cast<const _Float16*>(scales_of(k) + 256);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) *reinterpret_cast<f16x8*>(kbuf + ((wp * NS + 2 * wu + x) * 64 + lane) * 16) = kx[x] * ks8;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
+      vx[x] = expand8(lut, (uint32_t)vt[x], lane4);
       const _Float16* vs = vs_tab + (wu >> 1) * kTile + 32 * wp + 16 * x + 4 * half;
       const u32x2 lo = *reinterpret_cast<const u32x2*>(vs), hi = *reinterpret_cast<const u32x2*>(vs + 8);
-      const f16x8 vs8 = __builtin_bit_cast(f16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
-      *reinterpret_cast<f16x8*>(vbuf + (((wu * NP + wp) * 2 + x) * 64 + lane) * 16) =
-          expand8(lut, (uint32_t)t[x], lane4) * vs8;
+      vs8[x] = __builtin_bit_cast(f16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
     }
-    return meta;
+  };
+  auto stage_values = [&](int k) {
+    char* vbuf = smem + kPairBytes + (k & 1) * (2 * S::kOperand) + S::kOperand;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) *reinterpret_cast<f16x8*>(vbuf + (((wu * NP + wp) * 2 + x) * 64 + lane) * 16) = vx[x] * vs8[x];
   };
 
-  Meta meta{0, 0, false};
-  Raw raw;
-  uint32_t page = 0;
+  auto stage_all = [&](int k) {
+    stage_fetch(k + 1);
+    stage_keys(k + 1);
+    load_codes(k + 2);
+    stage_values(k + 1);
+  };
+
   if (tiles > 0) {                              // (a table without entries has no tiles)
-    const uint32_t p0 = find_page(0), p1 = find_page(1);
-    page = find_page(2);
-    const Raw first = load(0, p0);
-    raw = load(1, p1);
+    bool ok;
+    const int t = t0 + 16 * lane;
+    ahead = page_at(t);
+    scales_find(0);
     build_pairs<kThreads>(lv, lut);
+    found = row_at(t, ahead, ok);
+    load_codes(0);
+    scales_load(0);
+    scales_store(0);
     __syncthreads();
-    meta = stage(first, 0);
+    stage_fetch(0);
+    stage_keys(0);
+    stage_values(0);
+    load_codes(1);
     __syncthreads();
   }
 
@@ -256,21 +286,29 @@ __global__ void __launch_bounds__(kThreads, 2)
   float m = -INFINITY, l = 0.f;                 // m: reference of score + exponent of the tile's value scales
 
   for (int k = 0; k < tiles; ++k) {
-    const uint32_t page_now = page;
-    page = find_page(k + 3);
-    const Raw next = load(k + 2, page_now);
     const int pos0 = t0 + k * kTile;
-    const Meta now = meta;
+    const i32x4 meta = *reinterpret_cast<const i32x4*>(scales_of(k) + 512);
+    const int ek = __builtin_amdgcn_readfirstlane(meta[0]), ev = __builtin_amdgcn_readfirstlane(meta[1]);
+    const bool full = __builtin_amdgcn_readfirstlane(meta[2]) != 0;
+    // what comes once in a while: rows and scales of later tiles
+    if ((k + 2) % kKnown == kKnown / 2) ahead = page_at(t0 + ((k + 2) / kKnown + 1) * kKnown * kTile + 16 * lane);
+    if ((k + 2) % kKnown == 0) {
+      bool ok;
+      found = row_at(t0 + (k + 2) * kTile + 16 * lane, ahead, ok);
+    }
+    if ((k & 7) == 0) scales_find(k + 8);
+    if ((k & 7) == 2) scales_load(k + 8);
+    if ((k & 7) == 4) scales_store(k + 8);
+    const char* kbuf = smem + kPairBytes + (k & 1) * (2 * S::kOperand);
+    const char* vbuf = kbuf + S::kOperand;
     if (pos0 < any_high && pos0 + kTile > any_low) {
-      const char* kbuf = smem + kPairBytes + (k & 1) * (2 * S::kOperand);
-      const char* vbuf = kbuf + S::kOperand;
       f32x16 s[NP];
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[p][i] = 0.f;
       // operands are read kAhead products before their use
-      constexpr int kAhead = 4;
+      constexpr int kAhead = 2;
       f16x8 kf[kAhead];
       auto key = [&](int y) { return *reinterpret_cast<const f16x8*>(kbuf + ((y % NP * NS + y / NP) * 64 + lane) * 16); };
 #pragma unroll
@@ -280,14 +318,17 @@ __global__ void __launch_bounds__(kThreads, 2)
         const f16x8 now_k = kf[y % kAhead];
         if (y + kAhead < NP * NS) kf[y % kAhead] = key(y + kAhead);
         s[y % NP] = mfma32(now_k, q[y / NP], s[y % NP]);
+        if (D != 256 && y == 0) stage_fetch(k + 1);
+        if (D != 256 && y == NP * NS * 3 / 4) stage_keys(k + 1);
       }
-      if (!(now.full && pos0 >= all_low && pos0 + kTile <= all_high)) {
+      if (D != 256) load_codes(k + 2);
+      if (!(full && pos0 >= all_low && pos0 + kTile <= all_high)) {
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           uint32_t ok = 0xFFFFFFFFu;
-          if (!now.full) {                      // which positions are there
+          if (!full) {                      // which positions are there
             const int t = pos0 + 32 * p + col;
-            const uint32_t pg = (uint32_t)table[min((int)div_by((uint32_t)t, a.c.page_div), last)];
+            const uint32_t pg = (uint32_t)table[min((int)div_by((uint32_t)t, a.c.page_div), (int)a.table_width - 1)];
             ok = (uint32_t)__ballot(t < t1 && pg < a.c.pages);
           }
 #pragma unroll
@@ -297,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
       }
-      const float cf = factor * pow2(now.ek), fev = (float)now.ev;
+      const float cf = factor * pow2(ek), fev = (float)ev;
       float top = -INFINITY;
 #pragma unroll
       for (int p = 0; p < NP; ++p)
@@ -314,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int i = 0; i < 16; ++i) o[u][i] *= alpha;
         m = up;
       }
+
       const float base = fev - (m == -INFINITY ? 0.f : m);
       float sum = 0.f;
 #pragma unroll
@@ -321,24 +363,38 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           s[p][i] = exp2_fast(__builtin_fmaf(s[p][i], cf, base));
-          sum += s[p][i];
         }
-      l = __builtin_fmaf(sum, pow2(-now.ev), l);
+      f16x8 w[NP * 2];
 #pragma unroll
-      for (int p = 0; p < NP; ++p)
+      for (int y = 0; y < NP * 2; ++y) {
+        u32x4 h;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          u32x4 h;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) h[i] = pack_f16x2(s[p][8 * x + 2 * i], s[p][8 * x + 2 * i + 1]);
-          const f16x8 w = __builtin_bit_cast(f16x8, h);
-#pragma unroll
-          for (int u = 0; u < NU; ++u)
-            o[u] = mfma32(*reinterpret_cast<const f16x8*>(vbuf + (((u * NP + p) * 2 + x) * 64 + lane) * 16), w, o[u]);
+        for (int i = 0; i < 4; ++i) {
+          // (the sum takes the weights as they are: rounded to fp16 those of a tile whose
+          // value scales lie far below another's would weigh wrong in it)
+          const float w0 = s[y >> 1][8 * (y & 1) + 2 * i], w1 = s[y >> 1][8 * (y & 1) + 2 * i + 1];
+          sum += w0;
+          sum += w1;
+          h[i] = pack_f16x2(w0, w1);
         }
+        w[y] = __builtin_bit_cast(f16x8, h);
+      }
+      l = __builtin_fmaf(sum, pow2(-ev), l);
+      f16x8 vf[kAhead];
+      auto value = [&](int y) { return *reinterpret_cast<const f16x8*>(vbuf + ((y % NU * NP * 2 + y / NU) * 64 + lane) * 16); };
+#pragma unroll
+      for (int y = 0; y < kAhead; ++y) vf[y] = value(y);
+#pragma unroll
+      for (int y = 0; y < NU * NP * 2; ++y) {
+        const f16x8 now_v = vf[y % kAhead];
+        if (y + kAhead < NU * NP * 2) vf[y % kAhead] = value(y + kAhead);
+        o[y % NU] = mfma32(now_v, w[y / NU], o[y % NU]);
+        if (D != 256 && y == NU * NP) stage_values(k + 1);
+      }
+      if (D == 256) stage_all(k);
+    } else {
+      stage_all(k);
     }
-    if (k + 1 < tiles) meta = stage(raw, (k + 1) & 1);
-    raw = next;
     __syncthreads();
   }
 

@@ -150,7 +150,7 @@ def check(out, ref, spread, size, name):
 
 
 def run_case(seed, lengths, queries, Hkv, G, D, page, table, causal=True, window=0, uniform=False, gain=1.0,
-             max_len=None, poison=True, hide=None, strided=False, scale=None, spoil=None):
+             max_len=None, poison=True, hide=None, strided=False, scale=None, spoil=None, spike=None):
     """One attention call against the oracle.  Rows no sequence holds are poisoned with NaN scales.
     hide: (sequence, page) whose table entry is not a page.  spoil: (sequence, positions) stored as NaN."""
     rng = np.random.default_rng(seed)
@@ -176,6 +176,10 @@ def run_case(seed, lengths, queries, Hkv, G, D, page, table, causal=True, window
         for t in spoil[1]:
             for s in scales:
                 s[bt[spoil[0], t // page], :, t % page] = np.uint16(0x7FC0)
+    if spike is not None:                                     # (sequence 0's position, factor)
+        for s in scales:
+            r = s[bt[0, spike[0] // page], :, spike[0] % page]
+            s[bt[0, spike[0] // page], :, spike[0] % page] = kv_oracle.bf16_bits(kv_oracle.bits_f64(r) * spike[1])
     if hide is not None:
         bt[hide[0], hide[1]] = pages + 5
     starts = np.concatenate([[0], np.cumsum(queries)])
@@ -279,6 +283,15 @@ def test_non_finite_positions_reach_only_the_queries_that_see_them(D, n):
 @pytest.mark.parametrize("gain", [2.0 ** -90, 2.0 ** -20, 2.0 ** 12, 2.0 ** 60])
 def test_magnitudes(n, gain):
     run_case(1000 + n, [150, 61], [n, min(n, 61)], 1, 2, 128, 16, 0, gain=gain, scale=128 ** -0.5 / gain)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 90])
+def test_one_large_position(D, n):
+    """One position's scales far above the rest, wherever it lies in a tile."""
+    for at in (0, 5, 19, 37, 50, 77, 101, 140):
+        run_case(1050 + at, [150], [n], 1, 1, D, 16, 0, causal=False, spike=(at, 2.0 ** 18),
+                 scale=D ** -0.5 * 2.0 ** -18)
 
 
 def test_strides_and_other_streams():
