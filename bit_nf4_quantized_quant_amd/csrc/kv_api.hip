@@ -78,7 +78,7 @@ int check_attention(const qlora_kv_cache* c, int64_t q_heads, int64_t tokens, in
   if (st) return st;
   if (q_heads < 0 || tokens < 0 || seqs < 0 || max_q < 0 || max_len < 0 || window < 0) return QLORA_EINVAL;
   if (q_heads < 1 || q_heads % c->kv_heads || q_heads > kMaxHeads) return QLORA_ESHAPE;
-  if (tokens >= kMaxCount || max_len >= kMaxCount || max_q >= kMaxCount / q_heads || seqs > kMaxSeqs) return QLORA_ESHAPE;
+  if (tokens >= kMaxCount || max_len >= kMaxCount || max_q >= kMaxCount / 2 / q_heads || seqs > kMaxSeqs) return QLORA_ESHAPE;
   return QLORA_OK;
 }
 

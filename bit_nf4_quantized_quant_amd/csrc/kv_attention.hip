@@ -12,17 +12,63 @@ namespace qlora {
 namespace kv {
 namespace {
 
-// Joins the splits of one row a workgroup: D / 4 lanes hold four elements each,
-// and 1024 / D groups of them take the splits in turn.
-constexpr int kMaxSplits = 128;
+// One row's result from `splits` partial ones, by a workgroup of 256: partial s,
+// at row at(s) of o [rows][D] and stat [rows], holds exp2-weighted sums relative
+// to its own reference.  D / 4 lanes hold four elements each and 1024 / D groups
+// of them take the partials in turn, kChunk at a time.
+template <int D, typename At>
+__device__ __forceinline__ void join_row(int splits, At at, const float* o, const float2* stat, float inv_kappa,
+                                         uint16_t* out, float* lse) {
+  constexpr int kLanes = D / 4, kGroups = 256 / kLanes, kChunk = 256;
+  __shared__ float weight[kChunk];
+  __shared__ float wave_top[4], wave_sum[4];
+  __shared__ f32x4 acc[256];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // the common reference
+  float top = -INFINITY;
+  for (int s = tid; s < splits; s += kChunk) top = fmaxf(top, stat[at(s)].x);
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+  if (lane == 0) wave_top[wave] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
+  const float ref = top == -INFINITY ? 0.f : top;
+  const int g = tid / kLanes, col = tid % kLanes;
+  float sum = 0.f;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < splits; s0 += kChunk) {
+    const int count = min(kChunk, splits - s0);
+    __syncthreads();
+    if (tid < count) {
+      const float2 st = stat[at(s0 + tid)];
+      weight[tid] = exp2_fast(st.x - ref);
+      sum = __builtin_fmaf(weight[tid], st.y, sum);
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int s = g; s < count; s += kGroups) {
+      const float f = weight[s];
+      const f32x4 p = reinterpret_cast<const f32x4*>(o + at(s0 + s) * D)[col];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, p[e], v[e]);
+    }
+  }
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
+  if (lane == 0) wave_sum[wave] = sum;
+  acc[tid] = v;
+  __syncthreads();
+  if (tid >= kLanes) return;
+#pragma unroll
+  for (int h = 1; h < kGroups; ++h) v += acc[h * kLanes + tid];
+  sum = wave_sum[0] + wave_sum[1] + wave_sum[2] + wave_sum[3];
+  const float inv = sum == 0.f ? 0.f : inv_kappa / sum;
+  reinterpret_cast<u32x2*>(out)[tid] = u32x2{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
+  if (lse && tid == 0) *lse = sum == 0.f ? -INFINITY : kLn2 * (top + __builtin_amdgcn_logf(sum));
+}
 
 template <int D>
 __global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a, Split sp, float inv_kappa, Partial part) {
-  constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
-  __shared__ float weight[kMaxSplits];
-  __shared__ float2 total;
-  __shared__ f32x4 acc[256];
-  const int tid = threadIdx.x, lane = tid & 63;
   const int group = (int)a.q_heads / (int)a.c.heads;
   const int r = blockIdx.x % sp.rows, head = blockIdx.x / sp.rows, b = blockIdx.y;
   const Seq seq = sequence(a, b);
@@ -30,50 +76,10 @@ __global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a, Split sp, floa
   if (r >= rows) return;
   const int r0 = r / sp.tile_rows * sp.tile_rows;
   const Span span = tile_span(a, seq, r0 / group, (min(r0 + sp.tile_rows, rows) - 1) / group);
-  const int live = live_splits(span, sp.chunk, sp.splits);
   const int i = r / group;
   const int64_t row = (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
-  const int g = tid / kLanes, at = tid % kLanes;
-  const f32x4* o = reinterpret_cast<const f32x4*>(part.o + row * sp.splits * D) + at;
-  if (tid < 64) {
-    float2 st[kMaxSplits / 64];
-    float top = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int h = 0; h < kMaxSplits / 64; ++h) {
-      const int s = 64 * h + lane;
-      st[h] = s < live ? part.stat[row * sp.splits + s] : make_float2(-INFINITY, 0.f);
-      top = fmaxf(top, st[h].x);
-    }
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-    const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll
-    for (int h = 0; h < kMaxSplits / 64; ++h) {
-      const float f = exp2_fast(st[h].x - ref);
-      weight[64 * h + lane] = f;
-      sum = __builtin_fmaf(f, st[h].y, sum);
-    }
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
-    if (lane == 0) total = make_float2(top, sum);
-  }
-  __syncthreads();
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int s = g; s < live; s += kGroups) {
-    const float f = weight[s];
-    const f32x4 p = o[(int64_t)s * (D / 4)];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, p[e], v[e]);
-  }
-  acc[tid] = v;
-  __syncthreads();
-  if (tid >= kLanes) return;
-#pragma unroll
-  for (int h = 1; h < kGroups; ++h) v += acc[h * kLanes + tid];
-  const float top = total.x, sum = total.y, inv = sum == 0.f ? 0.f : inv_kappa / sum;
-  reinterpret_cast<u32x2*>(a.out + row * D)[tid] = u32x2{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
-  if (a.lse && tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : kLn2 * (top + __builtin_amdgcn_logf(sum));
+  join_row<D>(live_splits(span, sp.chunk, sp.splits), [&](int s) { return row * sp.splits + s; }, part.o, part.stat, inv_kappa,
+              a.out + row * D, a.lse ? a.lse + row : nullptr);
 }
 
 // fp32 -> fp16 bits, round to nearest even, for magnitudes of fp16's normal range (or 0).
@@ -103,14 +109,17 @@ const Levels& levels_of(int table) {
   return lv[table];
 }
 
+static int64_t span_bound(const AttnArgs& a) {
+  return std::max<int64_t>(1, a.window > 0 ? std::min(a.max_len, a.window + a.max_q + 15) : a.max_len);
+}
+
 Split split_of(const AttnArgs& a, int tile_rows, int fill, int least, int alone) {
+  constexpr int kMaxSplits = 128;
   Split s;
   s.rows = (int)(a.max_q * (a.q_heads / a.c.heads));
   s.tile_rows = tile_rows;
   s.tiles = (s.rows + tile_rows - 1) / tile_rows;
-  int64_t span = a.max_len;
-  if (a.window > 0) span = std::min(span, a.window + a.max_q + 15);
-  span = std::max<int64_t>(span, 1);
+  const int64_t span = span_bound(a);
   const int64_t groups = a.seqs * a.c.heads * s.tiles;
   const int64_t splits = std::min<int64_t>(std::max<int64_t>(1, fill / groups), kMaxSplits);
   const int64_t each = span <= alone ? span : std::max<int64_t>(least, (span + splits - 1) / splits);
