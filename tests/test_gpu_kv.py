@@ -373,6 +373,23 @@ def test_offsets_past_32_bits():
         check(bf16_f64(host_bf16_bits(out)), ref, spread, size, "far pages")
 
 
+def test_decoder_block_steps_match_one_prompt():
+    """The example's block: tokens taken one at a time against the whole sequence taken as one prompt.
+
+    Both see the same codes except where rounding in the projections differs by the path its row count takes: an
+    output of the q|k|v projection that lies within its rounding of a code's edge may take the next code.  With bf16
+    outputs (2^-9 relative rms) and 16 levels about 0.1 apart that is about one element in 30, each moved by about 0.1
+    of its run's scale, so a value moves by 2 % rms where it happens, 0.4 % on the whole; the o projection keeps
+    relative sizes.  Bound: 5 times that."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_attention.py")
+    spec = importlib.util.spec_from_file_location("decode_attention", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert example.run(seqs=2, prompt=150, steps=3) <= 2e-2
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_seeded_shapes(seed):
     rng = np.random.default_rng(9000 + seed)
