@@ -10,20 +10,21 @@
 namespace qlora {
 namespace kv {
 
-// n / d for 0 <= n < 2^31 and a fixed 2 <= d < 2^31 by one 32-bit multiply:
+// n / d for 0 <= n < 2^31 and a fixed 1 <= d < 2^31 by one 32-bit multiply:
 // with 2^b the smallest power of two >= d and m = ceil(2^(31+b) / d), which
 // fits 32 bits, m n / 2^(31+b) exceeds n / d by less than n / 2^(31+b) < 1 / d.
+// 2 n m / 2^32 is then shifted by b.
 struct FastDiv {
   uint32_t d, m, shift;
 };
 
 inline FastDiv fast_div(uint32_t d) {
-  uint32_t b = 1;
+  uint32_t b = 0;
   while ((uint64_t(1) << b) < d) ++b;
-  return FastDiv{d, (uint32_t)(((uint64_t(1) << (31 + b)) + d - 1) / d), b - 1};
+  return FastDiv{d, (uint32_t)(((uint64_t(1) << (31 + b)) + d - 1) / d), b};
 }
 
-__device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) { return __umulhi(n, f.m) >> f.shift; }
+__device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) { return __umulhi(2 * n, f.m) >> f.shift; }
 
 // One cache (device pointers); row (page heads + head) page_size + offset of a
 // codes tensor is D / 2 bytes long, of a scales tensor D / 64 bf16 numbers.
@@ -59,6 +60,7 @@ struct AttnArgs {
   int64_t token_stride, head_stride;
   int64_t tokens;
   int64_t q_heads;
+  FastDiv group_div;         // by q_heads / heads
   const int32_t* block_table;
   int64_t table_width;
   const int32_t* lengths;

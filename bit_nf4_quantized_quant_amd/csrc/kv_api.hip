@@ -135,6 +135,7 @@ size_t qlora_kv_attention_workspace(const qlora_kv_cache* cache, int64_t q_heads
   kv::AttnArgs a{};
   a.c = device_cache(cache);
   a.q_heads = q_heads;
+  a.group_div = kv::fast_div((uint32_t)(q_heads / cache->kv_heads));
   a.tokens = tokens;
   a.seqs = seqs;
   a.max_q = max_q;
@@ -169,6 +170,7 @@ int qlora_kv_attention(const qlora_kv_cache* cache, const uint16_t* q, const int
   a.head_stride = q_strides[1];
   a.tokens = tokens;
   a.q_heads = q_heads;
+  a.group_div = kv::fast_div((uint32_t)(q_heads / cache->kv_heads));
   a.block_table = block_table;
   a.table_width = table_width;
   a.lengths = lengths;

@@ -69,14 +69,14 @@ __device__ __forceinline__ void join_row(int splits, At at, const float* o, cons
 
 template <int D>
 __global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a, Split sp, float inv_kappa, Partial part) {
-  const int group = (int)a.q_heads / (int)a.c.heads;
+  const int group = (int)a.group_div.d;
   const int r = blockIdx.x % sp.rows, head = blockIdx.x / sp.rows, b = blockIdx.y;
   const Seq seq = sequence(a, b);
   const int rows = seq.n * group;
   if (r >= rows) return;
   const int r0 = r / sp.tile_rows * sp.tile_rows;
-  const Span span = tile_span(a, seq, r0 / group, (min(r0 + sp.tile_rows, rows) - 1) / group);
-  const int i = r / group;
+  const Span span = tile_span(a, seq, div_by(r0, a.group_div), div_by(min(r0 + sp.tile_rows, rows) - 1, a.group_div));
+  const int i = div_by(r, a.group_div);
   const int64_t row = (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
   join_row<D>(live_splits(span, sp.chunk, sp.splits), [&](int s) { return row * sp.splits + s; }, part.o, part.stat, inv_kappa,
               a.out + row * D, a.lse ? a.lse + row : nullptr);

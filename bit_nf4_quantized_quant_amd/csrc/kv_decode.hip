@@ -139,12 +139,17 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
   const int col = lane & 15, quad = lane >> 4;
   const int split = blockIdx.x % sp.splits, b = blockIdx.y;
   const int head = blockIdx.x / sp.splits / sp.tiles, r0 = blockIdx.x / sp.splits % sp.tiles * kRows;
-  const int group = (int)a.q_heads / (int)a.c.heads;
-  build_pairs<kThreads>(lv, lut);               // (while the sequence's numbers are on their way)
+  const int group = (int)a.group_div.d;
+  // the first pages are fetched, and the pair table is made, while the sequence's numbers
+  // are on their way: without a window the positions start at 0
+  const int32_t* table = a.block_table + (int64_t)b * a.table_width;
+  const int t_lane = split * sp.chunk + ((lane >> 1) * kWaves + wave) * kTile + (lane & 1) * 16;
+  const uint32_t early_page = a.table_width > 0 ? (uint32_t)table[min((int)div_by(t_lane, a.c.page_div), (int)a.table_width - 1)] : 0;
+  build_pairs<kThreads>(lv, lut);
   const Seq seq = sequence(a, b);
   const int rows = seq.n * group;
   if (r0 >= rows) return;
-  const int i_first = r0 / group, i_last = (min(r0 + kRows, rows) - 1) / group;
+  const int i_first = div_by(r0, a.group_div), i_last = div_by(min(r0 + kRows, rows) - 1, a.group_div);
   const Span span = tile_span(a, seq, i_first, i_last);
   const int live = live_splits(span, sp.chunk, sp.splits);
   if (split >= max(live, sp.splits == 1 ? 1 : 0)) return;
@@ -154,14 +159,13 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
   // this wave's tiles are tiles wave, wave + 8, ... of the chunk; lane 2 k + g holds
   // the cache row of group g of tile k of the next 32 of them, and a bit in `held`
   // that its page exists
-  const int32_t* table = a.block_table + (int64_t)b * a.table_width;
-  auto find_rows = [&](int first, uint64_t& held) -> uint32_t {
+  auto find_rows = [&](int first, bool early, uint64_t& held) -> uint32_t {
     const int t = t0 + ((first + (lane >> 1)) * kWaves + wave) * kTile + (lane & 1) * 16;
     uint32_t row = 0;
     bool ok = t < t1;
     if (ok) {
       const uint32_t pg = div_by((uint32_t)t, a.c.page_div);
-      const uint32_t page = (uint32_t)table[pg];
+      const uint32_t page = early ? early_page : (uint32_t)table[pg];
       ok = page < a.c.pages;
       if (ok) row = (page * a.c.heads + head) * a.c.page_size + ((uint32_t)t - pg * a.c.page_size);
     }
@@ -169,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
     return row;
   };
   uint64_t held;
-  uint32_t found = find_rows(0, held);
+  uint32_t found = find_rows(0, span.low == 0, held);
   auto tile_rows = [&](int k, uint32_t (&row)[2]) {
     row[0] = __builtin_amdgcn_readlane(found, 2 * (k & 31));
     row[1] = __builtin_amdgcn_readlane(found, 2 * (k & 31) + 1);
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
   int qlow[kNQ], qhigh[kNQ];
 #pragma unroll
   for (int j = 0; j < kNQ; ++j) {
-    const int r = min(r0 + 16 * j + col, rows - 1), i = r / group;
+    const int r = min(r0 + 16 * j + col, rows - 1), i = div_by(r, a.group_div);
     qlow[j] = seen_low(a, seq, i);
     qhigh[j] = seen_high(a, seq, i);
     const uint16_t* src = a.q + (int64_t)(seq.q0 + i) * a.token_stride +
@@ -246,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
     const uint32_t pages_ok = (uint32_t)(held >> (2 * (k & 31))) & 3u;
     bool whole = pos0 >= all_low && pos0 + kTile <= min(all_high, t1) && pages_ok == 3;
     if (k + 1 < mine) {                           // (the last tile's rows are loaded twice, into nothing)
-      if (((k + 1) & 31) == 0) found = find_rows(k + 1, held);
+      if (((k + 1) & 31) == 0) found = find_rows(k + 1, false, held);
       tile_rows(k + 1, row);
     }
     // value rows into LDS
@@ -413,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
       const float2 s = stats[(w * kNQ + j) * 16 + orow];
       rsum = __builtin_fmaf(exp2_fast(s.x - rref), s.y, rsum);
     }
-    const int i = r / group;
+    const int i = div_by(r, a.group_div);
     const int64_t out_row = (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
     const float inv = rsum == 0.f ? 0.f : lv.inv_kappa / rsum;
 #pragma unroll

@@ -103,11 +103,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   // the last row tiles of a causal prompt see most: they start first
   const int rest = blockIdx.x / sp.splits;
   const int head = rest % (int)a.c.heads, r0 = (sp.tiles - 1 - rest / (int)a.c.heads) * kRows;
-  const int group = (int)a.q_heads / (int)a.c.heads;
+  const int group = (int)a.group_div.d;
   const Seq seq = sequence(a, b);
   const int rows = seq.n * group;
   if (r0 >= rows) return;
-  const Span span = tile_span(a, seq, r0 / group, (min(r0 + kRows, rows) - 1) / group);
+  const Span span = tile_span(a, seq, div_by(r0, a.group_div), div_by(min(r0 + kRows, rows) - 1, a.group_div));
   const int live = live_splits(span, sp.chunk, sp.splits);
   if (split >= max(live, sp.splits == 1 ? 1 : 0)) return;
   const int t0 = span.low + split * sp.chunk;
@@ -117,10 +117,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   // ---- the queries of this wave: row w0 + col
   const int w0 = r0 + 32 * wave;
   const bool active = w0 < rows;
-  const int r = min(w0 + col, rows - 1), qi = r / group;
+  const int r = min(w0 + col, rows - 1), qi = div_by(r, a.group_div);
   const int qlow = seen_low(a, seq, qi), qhigh = seen_high(a, seq, qi);
   // positions that some, and that all, of the wave's rows see
-  const int i_first = min(w0, rows - 1) / group, i_last = (min(w0 + 32, rows) - 1) / group;
+  const int i_first = div_by(min(w0, rows - 1), a.group_div), i_last = div_by(min(w0 + 32, rows) - 1, a.group_div);
   const int any_low = seen_low(a, seq, i_first), any_high = active ? seen_high(a, seq, i_last) : 0;
   const int all_low = seen_low(a, seq, i_last), all_high = seen_high(a, seq, i_first);
   const int64_t out_row = (int64_t)(seq.q0 + qi) * a.q_heads + head * group + (r - qi * group);
