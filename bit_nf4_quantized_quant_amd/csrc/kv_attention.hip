@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "kv_common.h"
+#include "launch.h"
 
 namespace qlora {
 namespace kv {
@@ -109,44 +110,64 @@ const Levels& levels_of(int table) {
   return lv[table];
 }
 
-static int64_t span_bound(const AttnArgs& a) {
-  return std::max<int64_t>(1, a.window > 0 ? std::min(a.max_len, a.window + a.max_q + 15) : a.max_len);
-}
-
-Split split_of(const AttnArgs& a, int tile_rows, int fill, int least, int alone) {
+Split split_of(const AttnArgs& a, const Cost& cost, float* us) {
   constexpr int kMaxSplits = 128;
-  Split s;
-  s.rows = (int)(a.max_q * (a.q_heads / a.c.heads));
-  s.tile_rows = tile_rows;
-  s.tiles = (s.rows + tile_rows - 1) / tile_rows;
-  const int64_t span = span_bound(a);
-  const int64_t groups = a.seqs * a.c.heads * s.tiles;
-  const int64_t splits = std::min<int64_t>(std::max<int64_t>(1, fill / groups), kMaxSplits);
-  const int64_t each = span <= alone ? span : std::max<int64_t>(least, (span + splits - 1) / splits);
-  s.chunk = (int)((each + 255) / 256 * 256);
-  s.splits = (int)((span + s.chunk - 1) / s.chunk);
-  return s;
+  constexpr float kJoin = 6.f;              // the joining launch, us: 4 on the device, and the host's 3.5
+  constexpr float kJoinBytes = 4e6f;        // its bytes per us, written and read back
+  const int64_t rows = a.max_q * (a.q_heads / a.c.heads), tiles = (rows + cost.tile_rows - 1) / cost.tile_rows;
+  const int64_t pieces = a.seqs * a.c.heads * tiles;
+  const int64_t span = std::max<int64_t>(1, a.window > 0 ? std::min(a.max_len, a.window + a.max_q + 15) : a.max_len);
+  const int cus = cu_count();
+  Split best{};
+  *us = INFINITY;
+  for (int64_t n = 1; n <= kMaxSplits; n *= 2) {
+    const int64_t chunk = ((span + n - 1) / n + 255) / 256 * 256, splits = (span + chunk - 1) / chunk;
+    const int64_t groups = pieces * splits, slots = (int64_t)cost.per_cu * cus;
+    const float each = cost.base + (float)std::min(chunk, span) * (groups > cus ? cost.shared : cost.position);
+    const float joined = (float)a.tokens * a.q_heads * splits * a.c.D * 8.f;
+    const float t = (float)((groups + slots - 1) / slots) * each + (splits > 1 ? kJoin + joined / kJoinBytes : 0.f);
+    if (t < *us) {
+      *us = t;
+      best = Split{(int)chunk, (int)splits, (int)rows, (int)tiles, cost.tile_rows};
+    }
+    if (chunk == 256) break;
+  }
+  return best;
 }
 
 namespace {
 
-bool few_rows(const AttnArgs& a) { return a.max_q * (a.q_heads / a.c.heads) <= 64; }
+// The kernel for few rows shares a tile's expanded codes between 32 query rows (16 at
+// D = 256), that for many between 256, but its workgroup takes as long for one row as
+// for 256.  So the choice is by the estimated times: 256 rows on each of 32 heads and
+// 1000 positions, D = 128, take 19 us with the first and 40 us with the second (as 32
+// workgroups do not fill the device); 128 rows on 128 heads and 300 positions 25 us and
+// 16.5 us.
+struct Choice {
+  bool prompt;
+  Split split;
+};
 
-Split choose_split(const AttnArgs& a) { return few_rows(a) ? decode_split(a) : prompt_split(a); }
+Choice choose(const AttnArgs& a) {
+  float few = 0.f, many = 0.f;
+  const Split d = split_of(a, decode_cost(a), &few), p = split_of(a, prompt_cost(a), &many);
+  return many < few ? Choice{true, p} : Choice{false, d};
+}
 
 }  // namespace
 
 size_t kv_attention_workspace_bytes(const AttnArgs& a) {
-  const Split sp = choose_split(a);
+  const Split sp = choose(a).split;
   return sp.splits == 1 ? 0 : (size_t)(a.tokens * a.q_heads) * sp.splits * (a.c.D * sizeof(float) + sizeof(float2));
 }
 
 hipError_t launch_kv_attention(const AttnArgs& a, hipStream_t s) {
-  const Split sp = choose_split(a);
+  const Choice c = choose(a);
+  const Split& sp = c.split;
   Partial part;
   part.o = static_cast<float*>(a.workspace);
   part.stat = reinterpret_cast<float2*>(part.o + (size_t)(a.tokens * a.q_heads) * sp.splits * a.c.D);
-  const hipError_t e = few_rows(a) ? launch_decode(a, sp, part, s) : launch_prompt(a, sp, part, s);
+  const hipError_t e = c.prompt ? launch_prompt(a, sp, part, s) : launch_decode(a, sp, part, s);
   if (e != hipSuccess || sp.splits == 1) return e;
   const dim3 grid((unsigned)(sp.rows * a.c.heads), (unsigned)a.seqs);
   const auto kernel = a.c.D == 64 ? kv_join_kernel<64> : a.c.D == 128 ? kv_join_kernel<128> : kv_join_kernel<256>;

@@ -14,6 +14,8 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// A query's largest element as the products take it is below 2^(kQueryLift + 1).
+constexpr int kQueryLift = 12;
 
 // The 16 levels as the matrix products take them: fp16(kappa level), with
 // kappa the table's smallest factor that makes every level an fp16 number (15
@@ -37,14 +39,21 @@ struct Partial {
   float2* stat;  // [rows][splits]: reference, sum
 };
 
-// Splits such that about `fill` workgroups share the work, of at least
-// `least` positions each; up to `alone` positions are not split.
-Split split_of(const AttnArgs& a, int tile_rows, int fill, int least, int alone);
+// What a kernel's workgroups cost, in microseconds: to start and finish, and per
+// position that one walks through, alone on its CU or (`shared`) beside a second one.
+struct Cost {
+  int tile_rows;
+  int per_cu;              // workgroups that fit a CU
+  float base, position, shared;
+};
+
+// The split with the smallest estimated time, which goes to *us.
+Split split_of(const AttnArgs& a, const Cost& cost, float* us);
 
 // Attention for few query rows (kv_decode.hip) and for many (kv_prompt.hip).
-Split decode_split(const AttnArgs& a);
+Cost decode_cost(const AttnArgs& a);
 hipError_t launch_decode(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s);
-Split prompt_split(const AttnArgs& a);
+Cost prompt_cost(const AttnArgs& a);
 hipError_t launch_prompt(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s);
 
 // The queries of sequence b that a workgroup or a joining wave works on, and the

@@ -35,8 +35,11 @@ constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * 64;
 constexpr int kTile = 32;                       // positions per wave and step
 constexpr int kRound = kTile * kWaves;          // positions per workgroup and round
-constexpr int kMinEv = -100;                    // exponents of value scales below this count as this
-constexpr float kSlack = 8.f;                   // the reference is brought up to date once it is off by 2^8
+constexpr int kMinEv = -80;                    // exponents of value scales below this count as this
+// Weights x value scales enter the products as fp16 numbers up to 2^(kSlack + kLift + 1):
+// the reference is brought up to date once it is off by 2^kSlack, and lies 2^kLift below
+// the largest, so that positions with scales down to 2^-20 of the largest keep fp16's 11 bits.
+constexpr float kSlack = 6.f, kLift = 8.f;
 
 __device__ __forceinline__ f32x4 mfma16(const f16x8& a, const f16x8& b, const f32x4& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -188,8 +191,8 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
   load_scales<D>(cur.ks, a.c.scales[0], row, lane);
   load_scales<D>(cur.vs, a.c.scales[1], row, lane);
 
-  // the queries: row r0 + 16 j + col of the head's, each divided by the power of
-  // two of its largest element so that fp16 holds it
+  // the queries: row r0 + 16 j + col of the head's, its largest element
+  // brought to about 2^kQueryLift by a power of two so that fp16 holds it
   f16x8 q[kNQ][NB][2];
   float factor[kNQ];
   int qlow[kNQ], qhigh[kNQ];
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
         for (int x = 0; x < 4; ++x) top = max(top, max((raw[e][w][x] << 16) & 0x7FFFFFFFu, raw[e][w][x] & 0x7FFF0000u));
       }
     top = __float_as_uint(rows_max(__uint_as_float(min(top, 0x7E800000u))));
-    const int e2 = max((int)(top >> 23) - 127, -100);
+    const int e2 = max((int)(top >> 23) - 127, -100) - kQueryLift;
     // the sign of the score's factor goes into the queries, so that larger products are
     // larger scores
     const float down = a.scale > 0.f ? pow2(-e2) : a.scale < 0.f ? -pow2(-e2) : 0.f;
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
       for (int g = 0; g < 2; ++g)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, x[j][g][i]);
-      const float mn = __builtin_fmaf(rows_max(top), factor[j], fev);
+      const float mn = __builtin_fmaf(rows_max(top), factor[j], fev - kLift);
       if (__any(mn > m[j] + kSlack)) {
         const float up = fmaxf(m[j], mn);
         const float alpha = exp2_fast(m[j] - (up == -INFINITY ? 0.f : up));
@@ -359,8 +362,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
           l[j] += x[j][g][i];
         }
     }
-    // weights x value scales (at most 2^(kSlack + 1)), as the second operand of each
-    // run's products
+    // weights x value scales, as the second operand of each run's products
     f16x8 pv[kNQ][NB];
 #pragma unroll
     for (int e = 0; e < NB; ++e)
@@ -452,7 +454,10 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
   }
 }
 
-int tile_rows_of(const AttnArgs& a) { return a.max_q * (a.q_heads / a.c.heads) <= 16 ? 16 : 32; }
+// Rows of a tile.  Two groups of 16 share the expanded codes, but at D = 256 they do not
+// fit the registers: eight sequences of five queries on 32 of 4 heads, 4000 positions,
+// 101 us with two groups, 47 us with one.
+int tile_rows_of(const AttnArgs& a) { return a.c.D == 256 || a.max_q * (a.q_heads / a.c.heads) <= 16 ? 16 : 32; }
 
 template <int D, int kNQ>
 hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Partial& part, hipStream_t s) {
@@ -463,7 +468,15 @@ hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Pa
 
 }  // namespace
 
-Split decode_split(const AttnArgs& a) { return split_of(a, tile_rows_of(a), 512, 512, 1280); }
+// Measured with eight sequences of 1000 positions: 6 us and, a position, 6.2 and 10.5 ns at
+// D = 64 and 128 with 32 rows, 7.4 ns at D = 128 and 15.2 ns at D = 256 with 16; two
+// workgroups on a CU slow each other by about 1.4.
+Cost decode_cost(const AttnArgs& a) {
+  const int rows = tile_rows_of(a);
+  const float ns = a.c.D == 64 ? 6.2f : a.c.D == 256 ? 15.2f : rows == 16 ? 7.4f : 10.5f;
+  const int per_cu = a.c.D == 64 || (a.c.D == 128 && rows == 16) ? 2 : 1;
+  return Cost{rows, per_cu, 6.f, 1e-3f * ns, 1e-3f * ns * (per_cu == 2 ? 1.4f : 1.f)};
+}
 
 hipError_t launch_decode(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s) {
   const Levels& lv = levels_of(a.c.table);
@@ -471,7 +484,7 @@ hipError_t launch_decode(const AttnArgs& a, const Split& sp, const Partial& part
   switch (a.c.D) {
     case 64: return one ? launch<64, 1>(a, sp, lv, part, s) : launch<64, 2>(a, sp, lv, part, s);
     case 128: return one ? launch<128, 1>(a, sp, lv, part, s) : launch<128, 2>(a, sp, lv, part, s);
-    default: return one ? launch<256, 1>(a, sp, lv, part, s) : launch<256, 2>(a, sp, lv, part, s);
+    default: return launch<256, 1>(a, sp, lv, part, s);
   }
 }
 
