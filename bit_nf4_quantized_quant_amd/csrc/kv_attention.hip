@@ -3,8 +3,6 @@
 // joins the splits.
 #include <algorithm>
 #include <cmath>
-#include <cstring>
-#include <mutex>
 
 #include "kv_common.h"
 #include "launch.h"
@@ -83,32 +81,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a, Split sp, floa
               a.out + row * D, a.lse ? a.lse + row : nullptr);
 }
 
-// fp32 -> fp16 bits, round to nearest even, for magnitudes of fp16's normal range (or 0).
-uint32_t f16_bits(float f) {
-  uint32_t u;
-  std::memcpy(&u, &f, 4);
-  const uint32_t sign = (u >> 16) & 0x8000u;
-  u &= 0x7FFFFFFFu;
-  if (u == 0) return 0;
-  u += 0xFFFu + ((u >> 13) & 1u);
-  return sign | ((u >> 13) - (112u << 10));
-}
-
 }  // namespace
-
-const Levels& levels_of(int table) {
-  static Levels lv[kCodeTables];
-  static std::once_flag once;
-  std::call_once(once, [] {
-    for (int ty = 0; ty < kCodeTables; ++ty) {
-      // the uniform grid's levels are odd multiples of 1/15, FP4's are E2M1 numbers over 6
-      const float kappa = ty == kTableUniform4 ? 15.f : ty == kTableFp4 ? 3.f : 1.f;
-      lv[ty].inv_kappa = 1.0f / kappa;
-      for (int i = 0; i < 16; ++i) lv[ty].h[i] = f16_bits(kappa * code_table(ty).level[i]);
-    }
-  });
-  return lv[table];
-}
 
 Split split_of(const AttnArgs& a, const Cost& cost, float* us) {
   constexpr int kMaxSplits = 128;
@@ -171,7 +144,7 @@ hipError_t launch_kv_attention(const AttnArgs& a, hipStream_t s) {
   if (e != hipSuccess || sp.splits == 1) return e;
   const dim3 grid((unsigned)(sp.rows * a.c.heads), (unsigned)a.seqs);
   const auto kernel = a.c.D == 64 ? kv_join_kernel<64> : a.c.D == 128 ? kv_join_kernel<128> : kv_join_kernel<256>;
-  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, sp, levels_of(a.c.table).inv_kappa, part);
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, sp, fp16_levels(a.c.table).inv_kappa, part);
   return hipGetLastError();
 }
 

@@ -17,16 +17,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // A query's largest element as the products take it is below 2^(kQueryLift + 1).
 constexpr int kQueryLift = 12;
 
-// The 16 levels as the matrix products take them: fp16(kappa level), with
-// kappa the table's smallest factor that makes every level an fp16 number (15
-// for the uniform grid, 3 for FP4: both enter exactly) and 1 for NF4, whose
-// quantiles fp16 holds to 2^-11.
-struct Levels {
-  uint32_t h[16];
-  float inv_kappa;
-};
-
-const Levels& levels_of(int table);   // host; built once
+typedef Fp16Levels Levels;
 
 // How the positions of a row tile are cut, and where a split leaves the partial
 // result of row (token, head) if there are several.
@@ -141,7 +132,7 @@ constexpr int kPairBytes = 256 * 256;
 __device__ __forceinline__ uint32_t level_pair(const Levels& lv, uint32_t e) {
   int tab = 0;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) asm volatile("v_writelane_b32 %0, %1, %2" : "+v"(tab) : "s"(lv.h[k]), "n"(k));
+  for (int k = 0; k < 16; ++k) asm volatile("v_writelane_b32 %0, %1, %2" : "+v"(tab) : "s"(lv.bits[k]), "n"(k));
   const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute((int)((e & 15u) * 4u), tab);
   const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute((int)((e >> 4) * 4u), tab);
   return lo | (hi << 16);

@@ -479,7 +479,7 @@ Cost decode_cost(const AttnArgs& a) {
 }
 
 hipError_t launch_decode(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s) {
-  const Levels& lv = levels_of(a.c.table);
+  const Levels& lv = fp16_levels(a.c.table);
   const bool one = sp.tile_rows == 16;
   switch (a.c.D) {
     case 64: return one ? launch<64, 1>(a, sp, lv, part, s) : launch<64, 2>(a, sp, lv, part, s);

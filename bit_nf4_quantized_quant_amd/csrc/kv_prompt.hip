@@ -445,7 +445,7 @@ Cost prompt_cost(const AttnArgs& a) {
 }
 
 hipError_t launch_prompt(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s) {
-  const Levels& lv = levels_of(a.c.table);
+  const Levels& lv = fp16_levels(a.c.table);
   switch (a.c.D) {
     case 64: return launch<64>(a, sp, lv, part, s);
     case 128: return launch<128>(a, sp, lv, part, s);

@@ -215,4 +215,32 @@ const KvBuckets& kv_buckets(int type) {
   return bk[type];
 }
 
+namespace {
+
+// fp32 -> fp16 bits, round to nearest even, for magnitudes of fp16's normal range (or 0).
+uint32_t fp16_rne(float f) {
+  uint32_t u;
+  std::memcpy(&u, &f, 4);
+  const uint32_t sign = (u >> 16) & 0x8000u;
+  u &= 0x7FFFFFFFu;
+  if (u == 0) return 0;
+  u += 0xFFFu + ((u >> 13) & 1u);
+  return sign | ((u >> 13) - (112u << 10));
+}
+
+}  // namespace
+
+const Fp16Levels& fp16_levels(int type) {
+  static Fp16Levels lv[kCodeTables];
+  static std::once_flag once;
+  std::call_once(once, [] {
+    const float kappa[kCodeTables] = {1.7913437f, 15.0f, 3.0f};
+    for (int ty = 0; ty < kCodeTables; ++ty) {
+      lv[ty].inv_kappa = 1.0f / kappa[ty];
+      for (int i = 0; i < 16; ++i) lv[ty].bits[i] = fp16_rne((float)((double)kappa[ty] * code_table(ty).level[i]));
+    }
+  });
+  return lv[type];
+}
+
 }  // namespace qlora

@@ -68,4 +68,21 @@ struct DecodeLevels {
 
 const DecodeLevels& decode_levels(int type);
 
+// The levels as the cache's attention feeds them to fp16 matrix products:
+// fp16(kappa * L[i]), the products scaled by 1 / kappa at the end.  For the
+// uniform table kappa = 15 and for FP4 kappa = 3 make every level an fp16
+// number.  No factor does that for NF4's quantiles, and a mean over many
+// positions shrinks with their number while a mean rounding error of the levels
+// does not: at 131072 positions fp16(L) itself (mean error -1.1e-5 over the codes
+// that normal data take) puts the result 0.7 % off.  kappa = 1.7913437 leaves a
+// mean error of 1.2e-7 over the codes of normal data, and below 9e-7 over those of
+// Laplace, uniform and shifted normal data and over all codes alike; it is the
+// best of 2^20 factors in [1, 2) by the largest of these five.
+struct Fp16Levels {
+  uint32_t bits[16];
+  float inv_kappa;
+};
+
+const Fp16Levels& fp16_levels(int type);
+
 }  // namespace qlora

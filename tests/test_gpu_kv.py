@@ -260,6 +260,25 @@ def test_long_sequences(n):
     run_case(610 + n, [9001, 12], [n, min(n, 12)], 1, 2, 64, 256, 1, window=3000)
 
 
+@pytest.mark.parametrize("n", [1, 300])
+def test_very_long_context_of_stored_tokens(n):
+    """Over 262144 stored normal tokens a result is a few hundredths of the values it averages: an error of the levels
+    that has a mean over their codes would stand out against it."""
+    T, D, page = 262144, 64, 256
+    g = torch.Generator("cuda").manual_seed(11)
+    cache = qa.kv_cache(T // page, page, 1, D)
+    slots = torch.randperm(T // page, generator=g, device="cuda")[:, None] * page + torch.arange(page, device="cuda")
+    k, v = (torch.randn((T, 1, D), generator=g, device="cuda") for _ in range(2))
+    qa.kv_write(k, v, cache, slots.flatten().int())
+    k, v = (x.double()[:, 0] for x in qa.kv_read(cache, slots.flatten().int(), torch.float32))
+    q = torch.randn((n, 1, D), generator=g, device="cuda").bfloat16()
+    out, lse = qa.kv_attention(q, cache, (slots[:, 0] // page).int()[None], ints([T]), causal=False, want_lse=True)
+    score = q[:, 0].double() @ k.T.contiguous() * D ** -0.5
+    ref, rlse = torch.softmax(score, -1) @ v, torch.logsumexp(score, -1)
+    assert float((out[:, 0].double() - ref).norm() / ref.norm()) <= FRO_TOL
+    assert float((lse[:, 0].double() - rlse).abs().max()) <= 1e-4
+
+
 @pytest.mark.parametrize("n", [1, 80])
 def test_length_past_max_len_is_read_whole(n):
     run_case(700 + n, [900, 100], [n, n], 2, 1, 128, 16, 0, uniform=True, max_len=100)
