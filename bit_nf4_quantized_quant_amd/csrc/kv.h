@@ -76,8 +76,20 @@ struct AttnArgs {
 
 hipError_t launch_kv_write(const WriteArgs& a, hipStream_t s);
 hipError_t launch_kv_read(const ReadArgs& a, hipStream_t s);
-size_t kv_attention_workspace_bytes(const AttnArgs& a);
-hipError_t launch_kv_attention(const AttnArgs& a, hipStream_t s);
+
+// How the positions of a row tile are cut.
+struct Split {
+  int chunk, splits;           // positions per split, splits
+  int rows, tiles, tile_rows;  // query rows of a head at most, row tiles, rows of one
+};
+// Which kernel an attention call takes, its split, and the workspace it needs.
+struct AttnPlan {
+  bool prompt;
+  Split split;
+  size_t workspace;
+};
+AttnPlan kv_attention_plan(const AttnArgs& a);
+hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t s);
 
 }  // namespace kv
 }  // namespace qlora

@@ -1,7 +1,7 @@
 // C ABI of the 4-bit key/value cache: argument validation on the host, then
 // kernel launches on the caller's stream.  Every check runs before the first
-// HIP call.
-#include <algorithm>
+// launch.
+#include <cmath>
 
 #include "kv.h"
 #include "launch.h"
@@ -141,7 +141,7 @@ size_t qlora_kv_attention_workspace(const qlora_kv_cache* cache, int64_t q_heads
   a.max_q = max_q;
   a.max_len = max_len;
   a.window = window;
-  return kv::kv_attention_workspace_bytes(a);
+  return kv::kv_attention_plan(a).workspace;
 }
 
 int qlora_kv_attention(const qlora_kv_cache* cache, const uint16_t* q, const int64_t q_strides[2], int64_t tokens,
@@ -151,7 +151,7 @@ int qlora_kv_attention(const qlora_kv_cache* cache, const uint16_t* q, const int
                        void* stream) {
   int st = check_attention(cache, q_heads, tokens, seqs, max_q, max_len, window);
   if (st) return st;
-  if (table_width < 0) return QLORA_EINVAL;
+  if (table_width < 0 || !std::isfinite(scale)) return QLORA_EINVAL;
   // without q_starts every sequence has max_q queries
   if (!q_starts && (max_q == 0 ? tokens != 0 : tokens / max_q != seqs || tokens % max_q)) return QLORA_ESHAPE;
   if (tokens == 0 || seqs == 0 || max_q == 0) return QLORA_OK;
@@ -183,10 +183,10 @@ int qlora_kv_attention(const qlora_kv_cache* cache, const uint16_t* q, const int
   a.window = window;
   a.out = out;
   a.lse = lse;
-  const size_t need = kv::kv_attention_workspace_bytes(a);
-  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return QLORA_EINVAL;
+  const kv::AttnPlan plan = kv::kv_attention_plan(a);
+  if (plan.workspace > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < plan.workspace)) return QLORA_EINVAL;
   a.workspace = workspace;
-  return status_of(kv::launch_kv_attention(a, (hipStream_t)stream));
+  return status_of(kv::launch_kv_attention(a, plan, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -108,39 +108,27 @@ Split split_of(const AttnArgs& a, const Cost& cost, float* us) {
   return best;
 }
 
-namespace {
-
 // The kernel for few rows shares a tile's expanded codes between 32 query rows (16 at
 // D = 256), that for many between 256, but its workgroup takes as long for one row as
 // for 256.  So the choice is by the estimated times: 256 rows on each of 32 heads and
 // 1000 positions, D = 128, take 19 us with the first and 40 us with the second (as 32
 // workgroups do not fill the device); 128 rows on 128 heads and 300 positions 25 us and
 // 16.5 us.
-struct Choice {
-  bool prompt;
-  Split split;
-};
-
-Choice choose(const AttnArgs& a) {
+AttnPlan kv_attention_plan(const AttnArgs& a) {
   float few = 0.f, many = 0.f;
   const Split d = split_of(a, decode_cost(a), &few), p = split_of(a, prompt_cost(a), &many);
-  return many < few ? Choice{true, p} : Choice{false, d};
+  AttnPlan plan{many < few, many < few ? p : d, 0};
+  if (plan.split.splits > 1)
+    plan.workspace = (size_t)(a.tokens * a.q_heads) * plan.split.splits * (a.c.D * sizeof(float) + sizeof(float2));
+  return plan;
 }
 
-}  // namespace
-
-size_t kv_attention_workspace_bytes(const AttnArgs& a) {
-  const Split sp = choose(a).split;
-  return sp.splits == 1 ? 0 : (size_t)(a.tokens * a.q_heads) * sp.splits * (a.c.D * sizeof(float) + sizeof(float2));
-}
-
-hipError_t launch_kv_attention(const AttnArgs& a, hipStream_t s) {
-  const Choice c = choose(a);
-  const Split& sp = c.split;
+hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
+  const Split& sp = plan.split;
   Partial part;
   part.o = static_cast<float*>(a.workspace);
   part.stat = reinterpret_cast<float2*>(part.o + (size_t)(a.tokens * a.q_heads) * sp.splits * a.c.D);
-  const hipError_t e = c.prompt ? launch_prompt(a, sp, part, s) : launch_decode(a, sp, part, s);
+  const hipError_t e = plan.prompt ? launch_prompt(a, sp, part, s) : launch_decode(a, sp, part, s);
   if (e != hipSuccess || sp.splits == 1) return e;
   const dim3 grid((unsigned)(sp.rows * a.c.heads), (unsigned)a.seqs);
   const auto kernel = a.c.D == 64 ? kv_join_kernel<64> : a.c.D == 128 ? kv_join_kernel<128> : kv_join_kernel<256>;

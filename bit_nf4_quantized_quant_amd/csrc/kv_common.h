@@ -19,12 +19,7 @@ constexpr int kQueryLift = 12;
 
 typedef Fp16Levels Levels;
 
-// How the positions of a row tile are cut, and where a split leaves the partial
-// result of row (token, head) if there are several.
-struct Split {
-  int chunk, splits;           // positions per split, splits
-  int rows, tiles, tile_rows;  // query rows of a head at most, row tiles, rows of one
-};
+// Where a split leaves the partial result of row (token, head) if there are several.
 struct Partial {
   float* o;      // [rows][splits][D]
   float2* stat;  // [rows][splits]: reference, sum

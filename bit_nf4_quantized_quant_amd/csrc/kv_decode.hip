@@ -1,14 +1,21 @@
 // Attention over the 4-bit key/value cache for few query rows (gfx950): single
-// tokens and short runs of them, up to a few dozen rows (queries x heads of the
-// group) on one kv head.
+// tokens, short runs of them, and prompts too small to fill the device with the
+// kernel for many.  A row is a query of one head of the group.
 //
 //   out_i = sum_j softmax_j(scale q_i k_j) v_j
 //
-// What bounds it is the cache's bytes: each row is read once from HBM and its
-// codes are expanded in registers, by way of a table of level pairs in LDS,
-// straight into fp16 matrix operands.  The scales never touch the operands: a
-// key's scales multiply the scores of its 64-element runs after the product, a
-// value's multiply the softmax weights before it.
+// What bounds it is the cache's bytes on long contexts, and a workgroup's own
+// way (about 6 us, and 1.4 us a round of its waves) on short ones.  Each cache
+// row is read from HBM once and its codes are expanded in registers, by way of a
+// table of level pairs in LDS, straight into fp16 matrix operands.  The scales
+// never touch the operands: a key's scales multiply the scores of its 64-element
+// runs after the product, a value's multiply the softmax weights before it.
+//
+// Measured: two sequences of 131072 positions, 64 heads on 8 of 128: 63 us with
+// the joining, 285 MB at 4.5 TB/s (the kernel alone 58 us; in its middle it reads
+// 7 TB/s, the rest is the start and the joins); 32 sequences of 1 .. 4096
+// positions 32 us (2.3 TB/s: the longest sequences' workgroups walk twice the
+// mean); one sequence of 700, 32 heads 10.7 us.
 //
 // Split.  A workgroup takes one kv head, 16 kNQ query rows and a chunk of the
 // positions; its eight waves take tiles of 32 positions in turn, each with its
@@ -35,7 +42,7 @@ constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * 64;
 constexpr int kTile = 32;                       // positions per wave and step
 constexpr int kRound = kTile * kWaves;          // positions per workgroup and round
-constexpr int kMinEv = -80;                    // exponents of value scales below this count as this
+constexpr int kMinEv = -80;                     // exponents of value scales below this count as this
 // Weights x value scales enter the products as fp16 numbers up to 2^(kSlack + kLift + 1):
 // the reference is brought up to date once it is off by 2^kSlack, and lies 2^kLift below
 // the largest, so that positions with scales down to 2^-20 of the largest keep fp16's 11 bits.

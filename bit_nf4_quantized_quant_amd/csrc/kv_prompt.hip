@@ -3,15 +3,23 @@
 //
 //   out_i = sum_j softmax_j(scale q_i k_j) v_j
 //
-// What bounds it is the matrix cores together with the vector work of the
-// softmax.  A workgroup takes 256 query rows (queries x heads of the group) of
-// one kv head, 32 per wave, and walks the positions in tiles of 8192 / D.  The
-// codes of a tile are expanded once per workgroup, while the tile before it is
-// worked on: each wave turns an eighth of the keys and of the values into fp16
-// operands (level x scale, the scales divided by the power of two of the
-// tile's largest, which multiplies the scores and the weights instead) and
-// puts them in LDS in the order in which the products read them, 16 bytes a
-// lane.  The two buffers take 64 KiB, the table of level pairs another 64 KiB.
+// A workgroup takes 256 query rows (queries x heads of the group) of one kv head,
+// 32 per wave, and walks the positions in tiles of 8192 / D.  The codes of a tile
+// are expanded once per workgroup, while the tile before it is worked on: each
+// wave turns an eighth of the keys and of the values into fp16 operands (level x
+// scale, the scales brought to 2^10 by a power of two of the tile's, which
+// multiplies the scores and the weights instead) and puts them in LDS in the order
+// in which the products read them, 16 bytes a lane.  The two buffers take 64 KiB,
+// the table of level pairs another 64 KiB.  Every eight tiles a wave prepares the
+// scales of one of the next eight.
+//
+// What bounds it is a tile's way through a wave, about 2.2 us: 32 products (0.54 us
+// at the rate the card holds on a pure stream of them), twice that for the two waves
+// of a SIMD, 32 exponentials a lane, 32 KiB of operands from LDS a wave, an eighth of
+// the expansion; leaving any one out shortens it by no more than its own time.
+// Measured: the last 2048 tokens of 8192, 32 heads of 128: 271 us, 0.89 PFLOP/s of
+// 1.23 that a large library product reaches; six prompts of 1 .. 1500 tokens, 16 heads
+// on 4 of 256: 118 us, of which the longest workgroup's 47 tiles are 105.
 //
 // As with few rows, S^T = K Q^T (32x32x16 products: rows are positions, columns
 // are queries) leaves a lane with one query's scores, and the weights enter
@@ -28,7 +36,7 @@ namespace {
 constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * 64;
 constexpr int kRows = 32 * kWaves;              // query rows per workgroup
-constexpr int kMinExp = -80;                   // exponents of a tile's largest scales below this count as this
+constexpr int kMinExp = -80;                    // exponents of a tile's largest scales below this count as this
 // A tile's largest scale is brought to about 2^kScaleLift, weights lie below
 // 2^(kSlack + kLift): the reference is brought up to date once it is off by 2^kSlack, and
 // lies 2^kLift below the largest.  So what is 2^-20 of the largest keeps fp16's 11 bits.

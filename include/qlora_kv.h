@@ -63,8 +63,8 @@ typedef struct qlora_kv_cache {
  * bf16 (QLORA_KV_BF16) or fp32 (QLORA_KV_F32) by `dtype`, 16-byte aligned with
  * strides of whole 16-byte pieces; the strides are {token, head} of k, then of
  * v.  slots: int32 [tokens]; a token whose slot is negative or past the cache
- * is skipped (padding).  Two tokens of one call with the same slot leave either
- * one's runs there.
+ * is skipped (padding).  Two tokens of one call with the same slot leave an
+ * unspecified mixture of the two there.
  */
 int qlora_kv_write(const qlora_kv_cache* cache, const void* k, const void* v, int dtype, int64_t tokens,
                    const int64_t strides[4], const int32_t* slots, void* stream);
@@ -101,11 +101,17 @@ int qlora_kv_read(const qlora_kv_cache* cache, const int32_t* slots, int64_t tok
  * max_q and max_len bound the queries and the length of one sequence; they size
  * the launch.  Only a sequence's first max_q queries and only the positions
  * that table_width pages hold are computed with; a length beyond max_len is
- * still read whole, only slower.
+ * still read whole, only slower.  Rows of q in no sequence's run are not
+ * written in out and lse.  scale is finite.
  *
- * The scores and the sums are formed by fp16 matrix products of the levels
- * (fp16 holds them to 2^-12, with the scales applied in powers of two) with
- * fp32 accumulation; the softmax statistics are fp32.
+ * Rounding.  The products' operands are fp16 numbers, accumulated in fp32: the
+ * queries exactly (a row as it stands times a power of two; elements below 2^-26
+ * of its largest lose bits), the levels to 2^-11 (exactly for the uniform and
+ * FP4 tables; NF4's without a mean error), with few query rows the softmax
+ * weights times the values' scales, with many the weights, and levels times
+ * scales, to 2^-11 each.  Scales within a piece of up to 128 positions may span
+ * 2^20 before the smaller ones' products lose bits against the largest.  The
+ * softmax statistics and sums are fp32; out is rounded once to bf16.
  *
  * q: 16-byte aligned, strides {token, head} of whole 16-byte pieces.  out:
  * contiguous [tokens, q_heads, head_dim], 16-byte aligned.  workspace: at least

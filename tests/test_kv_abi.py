@@ -52,10 +52,10 @@ def read(c="good", slots=A, tokens=4, dtype=0, k=A, v=A):
 
 
 def attend(c="good", q=A, strides=(512, 128), tokens=4, heads=4, bt=A, width=2, lengths=A, starts=None, seqs=4, max_q=1,
-           max_len=32, window=0, out=A, lse=None, ws=A, ws_bytes=1 << 30):
+           max_len=32, window=0, out=A, lse=None, ws=A, ws_bytes=1 << 30, scale=0.1):
     s = None if strides is None else (ctypes.c_int64 * 2)(*strides)
     return _lib.lib().qlora_kv_attention(cache() if c == "good" else c, q, s, tokens, heads, bt, width, lengths, starts, seqs, max_q,
-                                         max_len, 0.1, 1, window, out, lse, ws, ws_bytes, None)
+                                         max_len, scale, 1, window, out, lse, ws, ws_bytes, None)
 
 
 @needs_lib
@@ -93,7 +93,7 @@ def test_attention_refusals():
     for kw in (dict(q=None), dict(q=MIS), dict(strides=None), dict(bt=None), dict(bt=A + 2), dict(lengths=None),
                dict(lengths=A + 1), dict(starts=A + 2), dict(out=None), dict(out=MIS), dict(lse=A + 2),
                dict(tokens=-1), dict(heads=-4), dict(seqs=-1), dict(max_q=-1), dict(max_len=-1), dict(window=-1),
-               dict(width=-1), dict(strides=(-512, 128))):
+               dict(width=-1), dict(strides=(-512, 128)), dict(scale=float("nan")), dict(scale=float("inf"))):
         assert attend(**kw) == EINVAL, kw
     for kw in (dict(heads=3), dict(heads=0), dict(heads=1 << 17), dict(strides=(516, 128)), dict(strides=(512, 1 << 40)),
                dict(tokens=5), dict(max_q=2), dict(max_q=0), dict(seqs=1 << 16, tokens=1 << 16), dict(max_len=1 << 31),
