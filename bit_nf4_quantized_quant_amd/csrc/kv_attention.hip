@@ -11,21 +11,81 @@ namespace qlora {
 namespace kv {
 namespace {
 
-// One row's result from `splits` partial ones, by a workgroup of 256: partial s,
-// at row at(s) of o [rows][D] and stat [rows], holds exp2-weighted sums relative
-// to its own reference.  D / 4 lanes hold four elements each and 1024 / D groups
-// of them take the partials in turn, kChunk at a time.
-template <int D, typename At>
-__device__ __forceinline__ void join_row(int splits, At at, const float* o, const float2* stat, float inv_kappa,
-                                         uint16_t* out, float* lse) {
+// out_r = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s over the splits s of a row, the
+// partial results relative to references m_s of their own.  Rows with one split are
+// written by the kernels themselves.
+//
+// Few splits, many rows: D / 4 lanes take a row, each four elements of it, and a
+// workgroup kJoinRows rows of a head, which lie in one row tile, in turn: most rows of a
+// ragged batch need no joining, and a workgroup for each costs more than the joins (32
+// sequences of 1 .. 4096 positions, 2048 rows of up to two splits: 5.6 us with a workgroup
+// a row, 3.9 us so).
+constexpr int kJoinRows = 16;
+
+template <int D>
+__global__ void __launch_bounds__(256) kv_join_rows_kernel(AttnArgs a, Split sp, float inv_kappa, Partial part) {
+  constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
+  const int group = (int)a.group_div.d, blocks = (sp.rows + kJoinRows - 1) / kJoinRows;
+  const int first = blockIdx.x % blocks * kJoinRows, head = blockIdx.x / blocks, b = blockIdx.y;
+  const Seq seq = sequence(a, b);
+  const int rows = seq.n * group;
+  if (first >= rows) return;
+  const int r0 = first / sp.tile_rows * sp.tile_rows;
+  const Span span = tile_span(a, seq, div_by(r0, a.group_div), div_by(min(r0 + sp.tile_rows, rows) - 1, a.group_div));
+  const int live = live_splits(span, sp.chunk, sp.splits);
+  if (live == 1) return;
+  const int col = threadIdx.x % kLanes;
+  for (int r = first + threadIdx.x / kLanes; r < min(first + kJoinRows, rows); r += kGroups) {
+    const int i = div_by(r, a.group_div);
+    const int64_t row = (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
+    const float2* stat = part.stat + row * sp.splits;
+    const f32x4* o = reinterpret_cast<const f32x4*>(part.o + row * sp.splits * D) + col;
+    float top = -INFINITY, sum = 0.f;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < live; ++s) top = fmaxf(top, stat[s].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll 2
+    for (int s = 0; s < live; ++s) {
+      const float2 st = stat[s];
+      const float f = exp2_fast(st.x - ref);
+      const f32x4 p = o[s * kLanes];
+      sum = __builtin_fmaf(f, st.y, sum);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, p[e], v[e]);
+    }
+    const float inv = sum == 0.f ? 0.f : inv_kappa / sum;
+    reinterpret_cast<u32x2*>(a.out + row * D)[col] =
+        u32x2{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
+    if (a.lse && col == 0) a.lse[row] = sum == 0.f ? -INFINITY : kLn2 * (top + __builtin_amdgcn_logf(sum));
+  }
+}
+
+// Many splits, few rows: a workgroup takes a row, D / 4 lanes four elements each, and
+// 1024 / D groups of lanes the splits in turn, kChunk at a time (two sequences of 131072
+// positions, 128 rows of 128 splits: 4.7 us; a wave a row 11.8 us).
+template <int D>
+__global__ void __launch_bounds__(256) kv_join_splits_kernel(AttnArgs a, Split sp, float inv_kappa, Partial part) {
   constexpr int kLanes = D / 4, kGroups = 256 / kLanes, kChunk = 256;
   __shared__ float weight[kChunk];
   __shared__ float wave_top[4], wave_sum[4];
   __shared__ f32x4 acc[256];
+  const int group = (int)a.group_div.d;
+  const int r = blockIdx.x % sp.rows, head = blockIdx.x / sp.rows, b = blockIdx.y;
+  const Seq seq = sequence(a, b);
+  const int rows = seq.n * group;
+  if (r >= rows) return;
+  const int r0 = r / sp.tile_rows * sp.tile_rows;
+  const Span span = tile_span(a, seq, div_by(r0, a.group_div), div_by(min(r0 + sp.tile_rows, rows) - 1, a.group_div));
+  const int splits = live_splits(span, sp.chunk, sp.splits);
+  if (splits == 1) return;
+  const int i = div_by(r, a.group_div);
+  const int64_t row = (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
+  const float2* stat = part.stat + row * sp.splits;
+  const f32x4* o = reinterpret_cast<const f32x4*>(part.o + row * sp.splits * D);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   // the common reference
   float top = -INFINITY;
-  for (int s = tid; s < splits; s += kChunk) top = fmaxf(top, stat[at(s)].x);
+  for (int s = tid; s < splits; s += kChunk) top = fmaxf(top, stat[s].x);
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
   if (lane == 0) wave_top[wave] = top;
@@ -39,7 +99,7 @@ __device__ __forceinline__ void join_row(int splits, At at, const float* o, cons
     const int count = min(kChunk, splits - s0);
     __syncthreads();
     if (tid < count) {
-      const float2 st = stat[at(s0 + tid)];
+      const float2 st = stat[s0 + tid];
       weight[tid] = exp2_fast(st.x - ref);
       sum = __builtin_fmaf(weight[tid], st.y, sum);
     }
@@ -47,7 +107,7 @@ __device__ __forceinline__ void join_row(int splits, At at, const float* o, cons
 #pragma unroll 4
     for (int s = g; s < count; s += kGroups) {
       const float f = weight[s];
-      const f32x4 p = reinterpret_cast<const f32x4*>(o + at(s0 + s) * D)[col];
+      const f32x4 p = o[(s0 + s) * kLanes + col];
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, p[e], v[e]);
     }
@@ -62,43 +122,58 @@ __device__ __forceinline__ void join_row(int splits, At at, const float* o, cons
   for (int h = 1; h < kGroups; ++h) v += acc[h * kLanes + tid];
   sum = wave_sum[0] + wave_sum[1] + wave_sum[2] + wave_sum[3];
   const float inv = sum == 0.f ? 0.f : inv_kappa / sum;
-  reinterpret_cast<u32x2*>(out)[tid] = u32x2{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
-  if (lse && tid == 0) *lse = sum == 0.f ? -INFINITY : kLn2 * (top + __builtin_amdgcn_logf(sum));
+  reinterpret_cast<u32x2*>(a.out + row * D)[tid] =
+      u32x2{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
+  if (a.lse && tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : kLn2 * (top + __builtin_amdgcn_logf(sum));
 }
 
+constexpr int kManySplits = 8;   // from here on a row has enough splits for a workgroup
+
 template <int D>
-__global__ void __launch_bounds__(256) kv_join_kernel(AttnArgs a, Split sp, float inv_kappa, Partial part) {
-  const int group = (int)a.group_div.d;
-  const int r = blockIdx.x % sp.rows, head = blockIdx.x / sp.rows, b = blockIdx.y;
-  const Seq seq = sequence(a, b);
-  const int rows = seq.n * group;
-  if (r >= rows) return;
-  const int r0 = r / sp.tile_rows * sp.tile_rows;
-  const Span span = tile_span(a, seq, div_by(r0, a.group_div), div_by(min(r0 + sp.tile_rows, rows) - 1, a.group_div));
-  const int i = div_by(r, a.group_div);
-  const int64_t row = (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
-  join_row<D>(live_splits(span, sp.chunk, sp.splits), [&](int s) { return row * sp.splits + s; }, part.o, part.stat, inv_kappa,
-              a.out + row * D, a.lse ? a.lse + row : nullptr);
+hipError_t launch_join(const AttnArgs& a, const Split& sp, float inv_kappa, const Partial& part, hipStream_t s) {
+  const int64_t rows = sp.splits < kManySplits ? (sp.rows + kJoinRows - 1) / kJoinRows : sp.rows;
+  const dim3 grid((unsigned)(rows * a.c.heads), (unsigned)a.seqs);
+  const auto kernel = sp.splits < kManySplits ? kv_join_rows_kernel<D> : kv_join_splits_kernel<D>;
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, sp, inv_kappa, part);
+  return hipGetLastError();
 }
 
 }  // namespace
 
+// The split whose estimated time is least.  Rows and lengths of the single sequences are
+// on the device; the estimate takes them to be spread evenly under max_q and max_len, with
+// the mean of the rows known from tokens, and rows to see the positions up to their own.
+// Unsplit workgroups of different lengths start longest first, so they take the longest
+// one's time or their mean load, whichever is more; pieces of one length go in rounds.
 Split split_of(const AttnArgs& a, const Cost& cost, float* us) {
   constexpr int kMaxSplits = 128;
   constexpr float kJoin = 6.f;              // the joining launch, us: 4 on the device, and the host's 3.5
   constexpr float kJoinBytes = 4e6f;        // its bytes per us, written and read back
-  const int64_t rows = a.max_q * (a.q_heads / a.c.heads), tiles = (rows + cost.tile_rows - 1) / cost.tile_rows;
-  const int64_t pieces = a.seqs * a.c.heads * tiles;
-  const int64_t span = std::max<int64_t>(1, a.window > 0 ? std::min(a.max_len, a.window + a.max_q + 15) : a.max_len);
+  const int64_t group = a.q_heads / a.c.heads, rows = a.max_q * group;
+  const int64_t tiles = (rows + cost.tile_rows - 1) / cost.tile_rows;
+  const int64_t tile_q = std::min<int64_t>(a.max_q, cost.tile_rows / group + 1);
+  const int64_t span = std::max<int64_t>(1, a.window > 0 ? std::min(a.max_len, a.window + tile_q + 15) : a.max_len);
+  const float mean_q = (float)a.tokens / (float)a.seqs, most_q = (float)std::min(a.max_q, a.max_len);
+  const float pieces = (float)a.c.heads * std::min((float)(a.seqs * tiles),
+                                                   (float)(a.tokens * group) / (float)cost.tile_rows + (float)a.seqs);
+  // positions that a tile sees: the mean, and the least
+  const float mean = std::min((float)span, std::max(1.f, (float)a.max_len - most_q + .25f * (mean_q + most_q)));
+  const float least = std::max(0.f, 2.f * mean - (float)span);
   const int cus = cu_count();
   Split best{};
   *us = INFINITY;
-  for (int64_t n = 1; n <= kMaxSplits; n *= 2) {
+  for (int64_t n = 1; n <= kMaxSplits; n = n == 1 ? 2 : n & (n - 1) ? n / 3 * 4 : n / 2 * 3) {   // 1, 2, 3, 4, 6, 8, 12 ..
     const int64_t chunk = ((span + n - 1) / n + 255) / 256 * 256, splits = (span + chunk - 1) / chunk;
-    const int64_t groups = pieces * splits, slots = (int64_t)cost.per_cu * cus;
-    const float each = cost.base + (float)std::min(chunk, span) * (groups > cus ? cost.shared : cost.position);
-    const float joined = (float)a.tokens * a.q_heads * splits * a.c.D * 8.f;
-    const float t = (float)((groups + slots - 1) / slots) * each + (splits > 1 ? kJoin + joined / kJoinBytes : 0.f);
+    const float cuts = splits == 1 ? 1.f : std::min((float)splits, std::max(1.f, mean / (float)chunk + .5f));
+    const float groups = pieces * cuts, rounds = groups / (float)(cost.per_cu * cus);
+    const float position = groups > (float)cus ? cost.shared : cost.position;
+    const float longest = cost.base + (float)std::min(chunk, span) * position;
+    float t = splits == 1 && 2.f * least < (float)span ? std::max(longest, rounds * (cost.base + mean * position))
+                                                       : std::ceil(rounds) * longest;
+    if (splits > 1) {
+      const float joined = ((float)span - std::max((float)chunk, least)) / std::max(1.f, (float)span - least);
+      t += kJoin + joined * (float)a.tokens * (float)a.q_heads * std::max(2.f, cuts) * (float)a.c.D * 8.f / kJoinBytes;
+    }
     if (t < *us) {
       *us = t;
       best = Split{(int)chunk, (int)splits, (int)rows, (int)tiles, cost.tile_rows};
@@ -130,10 +205,12 @@ hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& plan, hipStrea
   part.stat = reinterpret_cast<float2*>(part.o + (size_t)(a.tokens * a.q_heads) * sp.splits * a.c.D);
   const hipError_t e = plan.prompt ? launch_prompt(a, sp, part, s) : launch_decode(a, sp, part, s);
   if (e != hipSuccess || sp.splits == 1) return e;
-  const dim3 grid((unsigned)(sp.rows * a.c.heads), (unsigned)a.seqs);
-  const auto kernel = a.c.D == 64 ? kv_join_kernel<64> : a.c.D == 128 ? kv_join_kernel<128> : kv_join_kernel<256>;
-  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, sp, fp16_levels(a.c.table).inv_kappa, part);
-  return hipGetLastError();
+  const float inv_kappa = fp16_levels(a.c.table).inv_kappa;
+  switch (a.c.D) {
+    case 64: return launch_join<64>(a, sp, inv_kappa, part, s);
+    case 128: return launch_join<128>(a, sp, inv_kappa, part, s);
+    default: return launch_join<256>(a, sp, inv_kappa, part, s);
+  }
 }
 
 }  // namespace kv

@@ -88,8 +88,10 @@ __device__ __forceinline__ Span tile_span(const AttnArgs& a, const Seq& s, int i
   p.high = seen_high(a, s, i_last);
   return p;
 }
+// Splits of a tile that hold positions; at least one, which writes the result itself if
+// it is the only one.
 __device__ __forceinline__ int live_splits(const Span& p, int chunk, int splits) {
-  return p.high <= p.low ? 0 : min(splits, (p.high - p.low + chunk - 1) / chunk);
+  return p.high - p.low <= chunk ? 1 : min(splits, (p.high - p.low + chunk - 1) / chunk);
 }
 
 // Joined over the four 16-lane rows of a wave (rows differ, lanes of a column agree after it).

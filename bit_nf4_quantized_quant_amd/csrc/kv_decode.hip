@@ -14,7 +14,7 @@
 // Measured: two sequences of 131072 positions, 64 heads on 8 of 128: 63 us with
 // the joining, 285 MB at 4.5 TB/s (the kernel alone 58 us; in its middle it reads
 // 7 TB/s, the rest is the start and the joins); 32 sequences of 1 .. 4096
-// positions 32 us (2.3 TB/s: the longest sequences' workgroups walk twice the
+// positions 30 us (2.5 TB/s: the longest sequences' workgroups walk twice the
 // mean); one sequence of 700, 32 heads 10.7 us.
 //
 // Split.  A workgroup takes one kv head, 16 kNQ query rows and a chunk of the
@@ -147,7 +147,9 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
   char* lut = smem;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, quad = lane >> 4;
-  const int split = blockIdx.x % sp.splits, b = blockIdx.y;
+  // (neighbours go to different XCDs: with the split turned by the sequence none gets
+  // only the last splits, which short sequences do not have)
+  const int b = blockIdx.y, split = (blockIdx.x + b) % sp.splits;
   const int head = blockIdx.x / sp.splits / sp.tiles, r0 = blockIdx.x / sp.splits % sp.tiles * kRows;
   const int group = (int)a.group_div.d;
   // the first pages are fetched, and the pair table is made, while the sequence's numbers
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
   const int i_first = div_by(r0, a.group_div), i_last = div_by(min(r0 + kRows, rows) - 1, a.group_div);
   const Span span = tile_span(a, seq, i_first, i_last);
   const int live = live_splits(span, sp.chunk, sp.splits);
-  if (split >= max(live, sp.splits == 1 ? 1 : 0)) return;
+  if (split >= live) return;
   const int t0 = span.low + split * sp.chunk;
   const int t1 = split == sp.splits - 1 ? span.high : min(span.high, t0 + sp.chunk);
 
@@ -446,14 +448,14 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
         s.x += v.x, s.y += v.y;
       }
       if (r < rows) {
-        if (sp.splits == 1)
+        if (live == 1)
           reinterpret_cast<uint32_t*>(a.out + out_row * D + e * 64)[tid & 31] = pack_bf16x2(s.x * inv, s.y * inv);
         else
           reinterpret_cast<float2*>(part.o + (out_row * sp.splits + split) * D + e * 64)[tid & 31] = s;
       }
     }
     if (r < rows && (tid & 31) == 0) {
-      if (sp.splits > 1)
+      if (live > 1)
         part.stat[out_row * sp.splits + split] = make_float2(rtop, rsum);
       else if (a.lse)
         a.lse[out_row] = rsum == 0.f ? -INFINITY : kLn2 * (rtop + __builtin_amdgcn_logf(rsum));

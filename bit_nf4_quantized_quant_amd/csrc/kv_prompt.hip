@@ -18,8 +18,10 @@
 // of a SIMD, 32 exponentials a lane, 32 KiB of operands from LDS a wave, an eighth of
 // the expansion; leaving any one out shortens it by no more than its own time.
 // Measured: the last 2048 tokens of 8192, 32 heads of 128: 271 us, 0.89 PFLOP/s of
-// 1.23 that a large library product reaches; six prompts of 1 .. 1500 tokens, 16 heads
-// on 4 of 256: 118 us, of which the longest workgroup's 47 tiles are 105.
+// 1.23 that a large library product reaches; six prompts of 136 .. 1500 tokens, 16 heads
+// on 4 of 256: 108 us, of which the longest workgroup's 47 tiles are 98.  Queries and
+// results go through LDS to be read and written in whole rows: 16 bytes of 32 rows an
+// instruction took 4.7 and 3 to 7 us a workgroup, now 2 and 2 to 5.
 //
 // As with few rows, S^T = K Q^T (32x32x16 products: rows are positions, columns
 // are queries) leaves a lane with one query's scores, and the weights enter
@@ -61,6 +63,7 @@ struct Shape {
   static constexpr int kScaleOff = kRawOff + kWaves * 512;
   static constexpr int kScaleSize = 256 + 256 + 16;
   static constexpr size_t kBytes = kScaleOff + 16 * kScaleSize;
+  static_assert(kWaves * 16384 <= kBytes, "room for the waves' turned rows");
 };
 
 __device__ __forceinline__ float half_max(float v) {   // over a wave's two halves
@@ -71,6 +74,7 @@ __device__ __forceinline__ float half_add(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 // The exponents of the wave's largest finite bf16 numbers, two a lane in k and in v
 // (patterns of positive numbers order like the numbers; + 0x40 turns NaN negative).
 typedef short s16x2 __attribute__((ext_vector_type(2)));
@@ -102,6 +106,20 @@ __device__ __forceinline__ void top_exponents(uint32_t k, uint32_t v, int& ek, i
   ev = min(max(((max((int)(int16_t)(y >> 16), 0x40) - 0x40) >> 7) - 127, kMinExp), 126) - kScaleLift;
 }
 
+// Where a wave turns 32 rows of kChunks 16-byte chunks: a row's chunks one after the
+// other, the exclusive-or so that lanes reading a chunk of eight rows use all banks.
+constexpr int kTurn = 16384;
+template <int kChunks>
+__device__ __forceinline__ int turned(int row, int chunk) {
+  static_assert(kChunks % 8 == 0 && 32 * kChunks * 16 <= kTurn);
+  return (row * kChunks + (chunk ^ (row & 7))) * 16;
+}
+// Orders a wave's own LDS accesses (its lanes read what others of it wrote).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
     kv_prompt_kernel(AttnArgs a, Split sp, Levels lv, Partial part) {
@@ -111,22 +129,25 @@ __global__ void __launch_bounds__(kThreads, 2)
   char* lut = smem;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
-  const int split = blockIdx.x % sp.splits, b = blockIdx.y;
-  // the last row tiles of a causal prompt see most: they start first
-  const int rest = blockIdx.x / sp.splits;
-  const int head = rest % (int)a.c.heads, r0 = (sp.tiles - 1 - rest / (int)a.c.heads) * kRows;
+  // the last row tiles of a sequence see most: those of all sequences start first
+  const int rest = blockIdx.x / sp.splits, b = blockIdx.y;
+  const int head = rest % (int)a.c.heads, tile = rest / (int)a.c.heads * (int)gridDim.z + blockIdx.z;
+  // (neighbours go to different XCDs: with the split turned by the tile none gets only
+  // the last splits, which most tiles do not have)
+  const int split = (blockIdx.x + blockIdx.z) % sp.splits;
   const int group = (int)a.group_div.d;
   const Seq seq = sequence(a, b);
   const int rows = seq.n * group;
-  if (r0 >= rows) return;
+  const int r0 = ((rows + kRows - 1) / kRows - 1 - tile) * kRows;
+  if (r0 < 0) return;
   const Span span = tile_span(a, seq, div_by(r0, a.group_div), div_by(min(r0 + kRows, rows) - 1, a.group_div));
   const int live = live_splits(span, sp.chunk, sp.splits);
-  if (split >= max(live, sp.splits == 1 ? 1 : 0)) return;
+  if (split >= live) return;
   const int t0 = span.low + split * sp.chunk;
   const int t1 = split == sp.splits - 1 ? span.high : min(span.high, t0 + sp.chunk);
   const int tiles = t1 > t0 ? (t1 - t0 + kTile - 1) / kTile : 0;
 
-  // ---- the queries of this wave: row w0 + col
+  // ---- the rows of this wave: w0 + col
   const int w0 = r0 + 32 * wave;
   const bool active = w0 < rows;
   const int r = min(w0 + col, rows - 1), qi = div_by(r, a.group_div);
@@ -135,35 +156,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int i_first = div_by(min(w0, rows - 1), a.group_div), i_last = div_by(min(w0 + 32, rows) - 1, a.group_div);
   const int any_low = seen_low(a, seq, i_first), any_high = active ? seen_high(a, seq, i_last) : 0;
   const int all_low = seen_low(a, seq, i_last), all_high = seen_high(a, seq, i_first);
-  const int64_t out_row = (int64_t)(seq.q0 + qi) * a.q_heads + head * group + (r - qi * group);
-  f16x8 q[NS];                                  // step s: elements 32 (s / 2) + 16 half + 8 (s % 2) ..
-  float factor;
-  {
-    const uint16_t* src = a.q + (int64_t)(seq.q0 + qi) * a.token_stride +
-                          (int64_t)(head * group + (r - qi * group)) * a.head_stride + half * 16;
-    u32x4 raw[NS];
-    uint32_t top = 0;
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      raw[s] = *reinterpret_cast<const u32x4*>(src + 32 * (s >> 1) + 8 * (s & 1));
-#pragma unroll
-      for (int x = 0; x < 4; ++x) top = max(top, max((raw[s][x] << 16) & 0x7FFFFFFFu, raw[s][x] & 0x7FFF0000u));
-    }
-    top = __float_as_uint(half_max(__uint_as_float(min(top, 0x7E800000u))));
-    const int e2 = max((int)(top >> 23) - 127, -100) - kQueryLift;
-    // the sign of the score's factor goes into the queries, so that larger products are
-    // larger scores
-    const float down = a.scale > 0.f ? pow2(-e2) : a.scale < 0.f ? -pow2(-e2) : 0.f;
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      u32x4 h;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) h[x] = pack_f16x2(bf16_lo(raw[s][x]) * down, bf16_hi(raw[s][x]) * down);
-      q[s] = __builtin_bit_cast(f16x8, h);
-    }
-    factor = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * (kLog2e * lv.inv_kappa) * pow2(e2);
-  }
-
   // ---- a tile's way into LDS
   const int32_t* table = a.block_table + (int64_t)b * a.table_width;
   const int wp = wave / NU, wu = wave % NU;     // this wave's part of the positions and of the elements
@@ -272,15 +264,66 @@ __global__ void __launch_bounds__(kThreads, 2)
     stage_values(k + 1);
   };
 
+  // ---- the queries.  They come in whole rows, are turned in LDS and become operands of
+  // their row's lanes, the largest element brought to about 2^kQueryLift by a power of two
+  // so that fp16 holds it.  The first tile's pages, codes and scales come meanwhile.
   if (tiles > 0) {                              // (a table without entries has no tiles)
-    bool ok;
-    const int t = t0 + 16 * lane;
-    ahead = page_at(t);
+    ahead = page_at(t0 + 16 * lane);
     scales_find(0);
+  }
+  char* turn = smem + wave * kTurn;
+  f16x8 q[NS];                                  // step s: elements 32 (s / 2) + 16 half + 8 (s % 2) ..
+  float factor;
+  {
+    constexpr int kChunks = D / 8, kLoad = 64 / kChunks;   // chunks of a row, rows of a load
+    u32x4 raw[NS];
+    const uint64_t mine = (uint64_t)((int64_t)(seq.q0 + qi) * a.token_stride +      // where the lane's row begins
+                                     (int64_t)(head * group + (r - qi * group)) * a.head_stride);
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      const int row = j * kLoad + lane / kChunks;
+      const uint64_t at = (uint64_t)(uint32_t)__shfl((int)(mine >> 32), row) << 32 | (uint32_t)__shfl((int)mine, row);
+      raw[j] = *reinterpret_cast<const u32x4*>(a.q + at + lane % kChunks * 8);
+    }
+    if (tiles > 0) {
+      bool ok;
+      found = row_at(t0 + 16 * lane, ahead, ok);
+      load_codes(0);
+      scales_load(0);
+    }
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+      *reinterpret_cast<u32x4*>(turn + turned<kChunks>(j * kLoad + lane / kChunks, lane % kChunks)) = raw[j];
+    wave_sync();
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 tops = {0, 0};                        // (patterns of positive bf16 numbers order like the numbers)
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      raw[s] = *reinterpret_cast<const u32x4*>(turn + turned<kChunks>(col, 4 * (s >> 1) + 2 * half + (s & 1)));
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t w = raw[s][x] & 0x7FFF7FFFu;
+        tops = __builtin_elementwise_max(tops, __builtin_bit_cast(u16x2, w));
+      }
+    }
+    const uint32_t top = __float_as_uint(half_max(__uint_as_float(min((uint32_t)max(tops[0], tops[1]) << 16, 0x7E800000u))));
+    const int e2 = max((int)(top >> 23) - 127, -100) - kQueryLift;
+    // the sign of the score's factor goes into the queries, so that larger products are
+    // larger scores
+    const float down = a.scale > 0.f ? pow2(-e2) : a.scale < 0.f ? -pow2(-e2) : 0.f;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      u32x4 h;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) h[x] = pack_f16x2(bf16_lo(raw[s][x]) * down, bf16_hi(raw[s][x]) * down);
+      q[s] = __builtin_bit_cast(f16x8, h);
+    }
+    factor = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * (kLog2e * lv.inv_kappa) * pow2(e2);
+  }
+  __syncthreads();                              // (the pair table takes the place of the turned rows)
+
+  if (tiles > 0) {
     build_pairs<kThreads>(lv, lut);
-    found = row_at(t, ahead, ok);
-    load_codes(0);
-    scales_load(0);
     scales_store(0);
     __syncthreads();
     stage_fetch(0);
@@ -343,11 +386,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint32_t pg = (uint32_t)table[min((int)div_by((uint32_t)t, a.c.page_div), (int)a.table_width - 1)];
             ok = (uint32_t)__ballot(t < t1 && pg < a.c.pages);
           }
+          // bit n: the lane's row sees position `first` + n
+          const int first = pos0 + 32 * p + 4 * half;
+          const uint32_t see = bits_below(qhigh - first) & ~bits_below(qlow - first) & (ok >> (4 * half));
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int at = 8 * (i >> 2) + 4 * half + (i & 3), pos = pos0 + 32 * p + at;
-            if (!(pos >= qlow && pos < qhigh && ((ok >> at) & 1u))) s[p][i] = -INFINITY;
-          }
+          for (int i = 0; i < 16; ++i)
+            if (!((see >> (8 * (i >> 2) + (i & 3))) & 1u)) s[p][i] = -INFINITY;
         }
       }
       const float cf = factor * pow2(ek), fev = (float)ev;
@@ -410,35 +454,66 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
   }
 
-  // ---- out: lane (col, half) holds elements 32 u + 8 x + 4 half .. + 3 of row w0 + col
+  // ---- out: lane (col, half) holds elements 32 u + 8 x + 4 half .. + 3 of row w0 + col,
+  // which go through LDS into whole rows (lanes past the last row write it again)
+  if (!active) return;
   l = half_add(l);
-  if (w0 + col >= rows) return;
-  if (sp.splits > 1) {
-    float* dst = part.o + (out_row * sp.splits + split) * D + 4 * half;
+  const float inv = l == 0.f ? 0.f : lv.inv_kappa / l;
+  int me = lane;
+  asm volatile("" : "+v"(me));                  // what follows is not worth registers during the loop
+  const int my_row = me & 31, my_half = me >> 5;
+  auto row_of = [&](int r) -> int64_t {         // of the output and of the statistics
+    const int i = div_by(r, a.group_div);
+    return (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
+  };
+  if (live > 1) {
+    constexpr int kPart = D == 64 ? 64 : 128, kChunks = kPart / 4, kStore = 64 / kChunks;   // elements a pass
 #pragma unroll
-    for (int u = 0; u < NU; ++u)
+    for (int e = 0; e < D; e += kPart) {
+      wave_sync();
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        *reinterpret_cast<f32x4*>(dst + 32 * u + 8 * x) =
-            f32x4{o[u][4 * x], o[u][4 * x + 1], o[u][4 * x + 2], o[u][4 * x + 3]};
-    if (half == 0) part.stat[out_row * sp.splits + split] = make_float2(m, l);
+      for (int u = 0; u < kPart / 32; ++u)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const f32x16& v = o[e / 32 + u];
+          *reinterpret_cast<f32x4*>(turn + turned<kChunks>(my_row, 8 * u + 2 * x + my_half)) =
+              f32x4{v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]};
+        }
+      wave_sync();
+#pragma unroll 4
+      for (int j = 0; j < 32 / kStore; ++j) {
+        const int r = min(w0 + j * kStore + me / kChunks, rows - 1);
+        *reinterpret_cast<f32x4*>(part.o + (row_of(r) * sp.splits + split) * D + e + me % kChunks * 4) =
+            *reinterpret_cast<const f32x4*>(turn + turned<kChunks>(r - w0, me % kChunks));
+      }
+    }
+    if (my_half == 0 && w0 + my_row < rows) part.stat[row_of(w0 + my_row) * sp.splits + split] = make_float2(m, l);
   } else {
-    const float inv = l == 0.f ? 0.f : lv.inv_kappa / l;
-    uint16_t* dst = a.out + out_row * D + 4 * half;
+    constexpr int kChunks = D / 8, kStore = 64 / kChunks;
 #pragma unroll
     for (int u = 0; u < NU; ++u)
 #pragma unroll
       for (int x = 0; x < 4; ++x)
-        *reinterpret_cast<u32x2*>(dst + 32 * u + 8 * x) = u32x2{pack_bf16x2(o[u][4 * x] * inv, o[u][4 * x + 1] * inv),
-                                                                pack_bf16x2(o[u][4 * x + 2] * inv, o[u][4 * x + 3] * inv)};
-    if (a.lse && half == 0) a.lse[out_row] = l == 0.f ? -INFINITY : kLn2 * (m + __builtin_amdgcn_logf(l));
+        *reinterpret_cast<u32x2*>(turn + turned<kChunks>(my_row, 4 * u + x) + 8 * my_half) =
+            u32x2{pack_bf16x2(o[u][4 * x] * inv, o[u][4 * x + 1] * inv),
+                  pack_bf16x2(o[u][4 * x + 2] * inv, o[u][4 * x + 3] * inv)};
+    wave_sync();
+#pragma unroll 4
+    for (int j = 0; j < 32 / kStore; ++j) {
+      const int r = min(w0 + j * kStore + me / kChunks, rows - 1);
+      *reinterpret_cast<u32x4*>(a.out + row_of(r) * D + me % kChunks * 8) =
+          *reinterpret_cast<const u32x4*>(turn + turned<kChunks>(r - w0, me % kChunks));
+    }
+    if (a.lse && my_half == 0 && w0 + my_row < rows)
+      a.lse[row_of(w0 + my_row)] = l == 0.f ? -INFINITY : kLn2 * (m + __builtin_amdgcn_logf(l));
   }
 }
 
 template <int D>
 hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Partial& part, hipStream_t s) {
-  hipLaunchKernelGGL(kv_prompt_kernel<D>, dim3((unsigned)(sp.splits * sp.tiles * a.c.heads), (unsigned)a.seqs),
-                     dim3(kThreads), 0, s, a, sp, lv, part);
+  const int z = std::min(sp.tiles, 32768);      // (a grid's y and z end at 65535)
+  const dim3 grid((unsigned)(sp.splits * a.c.heads * ((sp.tiles + z - 1) / z)), (unsigned)a.seqs, (unsigned)z);
+  hipLaunchKernelGGL(kv_prompt_kernel<D>, grid, dim3(kThreads), 0, s, a, sp, lv, part);
   return hipGetLastError();
 }
 
