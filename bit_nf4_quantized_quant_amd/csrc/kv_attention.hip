@@ -183,16 +183,20 @@ Split split_of(const AttnArgs& a, const Cost& cost, float* us) {
   return best;
 }
 
-// The kernel for few rows shares a tile's expanded codes between 32 query rows (16 at
-// D = 256), that for many between 256, but its workgroup takes as long for one row as
-// for 256.  So the choice is by the estimated times: 256 rows on each of 32 heads and
-// 1000 positions, D = 128, take 19 us with the first and 40 us with the second (as 32
-// workgroups do not fill the device); 128 rows on 128 heads and 300 positions 25 us and
-// 16.5 us.
+// The kernel for few rows shares a tile's expanded codes between 16 or 32 query rows, that
+// for many between 256, but its workgroup takes as long for one row as for 256.  So the
+// choice is by the estimated times: 256 rows on each of 32 heads and 1000 positions, D =
+// 128, take 19 us with the first and 40 us with the second (as 32 workgroups do not fill
+// the device); 128 rows on 128 heads and 300 positions 25 us and 16.5 us.
 AttnPlan kv_attention_plan(const AttnArgs& a) {
-  float few = 0.f, many = 0.f;
-  const Split d = split_of(a, decode_cost(a), &few), p = split_of(a, prompt_cost(a), &many);
-  AttnPlan plan{many < few, many < few ? p : d, 0};
+  float least = 0.f, us = 0.f;
+  AttnPlan plan{false, split_of(a, decode_cost(a, 16), &least), 0};
+  if (a.c.D < 256 && plan.split.rows > 16) {
+    const Split s = split_of(a, decode_cost(a, 32), &us);
+    if (us < least) plan.split = s, least = us;
+  }
+  const Split s = split_of(a, prompt_cost(a), &us);
+  if (us < least) plan.split = s, plan.prompt = true;
   if (plan.split.splits > 1)
     plan.workspace = (size_t)(a.tokens * a.q_heads) * plan.split.splits * (a.c.D * sizeof(float) + sizeof(float2));
   return plan;

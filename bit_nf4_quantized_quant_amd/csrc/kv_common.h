@@ -37,7 +37,7 @@ struct Cost {
 Split split_of(const AttnArgs& a, const Cost& cost, float* us);
 
 // Attention for few query rows (kv_decode.hip) and for many (kv_prompt.hip).
-Cost decode_cost(const AttnArgs& a);
+Cost decode_cost(const AttnArgs& a, int rows);   // rows: 16, or 32 (D < 256)
 hipError_t launch_decode(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s);
 Cost prompt_cost(const AttnArgs& a);
 hipError_t launch_prompt(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s);
