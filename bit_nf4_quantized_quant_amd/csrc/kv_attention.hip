@@ -143,12 +143,13 @@ hipError_t launch_join(const AttnArgs& a, const Split& sp, float inv_kappa, cons
 // The split whose estimated time is least.  Rows and lengths of the single sequences are
 // on the device; the estimate takes them to be spread evenly under max_q and max_len, with
 // the mean of the rows known from tokens, and rows to see the positions up to their own.
-// Unsplit workgroups of different lengths start longest first, so they take the longest
-// one's time or their mean load, whichever is more; pieces of one length go in rounds.
+// Unsplit workgroups of different lengths take the longest one's time, or their mean load
+// and half the longest one's time if that is more; pieces of one length go in rounds.
 Split split_of(const AttnArgs& a, const Cost& cost, float* us) {
   constexpr int kMaxSplits = 128;
+  constexpr float kShared = 1.5f, kSharedBase = 1.3f;   // by which two workgroups on a CU slow each other
   constexpr float kJoin = 6.f;              // the joining launch, us: 4 on the device, and the host's 3.5
-  constexpr float kJoinBytes = 4e6f;        // its bytes per us, written and read back
+  constexpr float kJoinBytes = 6e6f;        // its bytes per us, written and read back
   const int64_t group = a.q_heads / a.c.heads, rows = a.max_q * group;
   const int64_t tiles = (rows + cost.tile_rows - 1) / cost.tile_rows;
   const int64_t tile_q = std::min<int64_t>(a.max_q, cost.tile_rows / group + 1);
@@ -166,10 +167,12 @@ Split split_of(const AttnArgs& a, const Cost& cost, float* us) {
     const int64_t chunk = ((span + n - 1) / n + 255) / 256 * 256, splits = (span + chunk - 1) / chunk;
     const float cuts = splits == 1 ? 1.f : std::min((float)splits, std::max(1.f, mean / (float)chunk + .5f));
     const float groups = pieces * cuts, rounds = groups / (float)(cost.per_cu * cus);
-    const float position = groups > (float)cus ? cost.shared : cost.position;
-    const float longest = cost.base + (float)std::min(chunk, span) * position;
-    float t = splits == 1 && 2.f * least < (float)span ? std::max(longest, rounds * (cost.base + mean * position))
-                                                       : std::ceil(rounds) * longest;
+    const bool shared = groups > (float)cus && cost.per_cu > 1;
+    const float position = (shared ? kShared : 1.f) * cost.position, base = (shared ? kSharedBase : 1.f) * cost.base;
+    const float longest = base + (float)std::min(chunk, span) * position;
+    float t = splits == 1 && 2.f * least < (float)span
+                  ? std::max(longest, rounds * (base + mean * position) + .5f * longest)
+                  : std::ceil(rounds) * longest;
     if (splits > 1) {
       const float joined = ((float)span - std::max((float)chunk, least)) / std::max(1.f, (float)span - least);
       t += kJoin + joined * (float)a.tokens * (float)a.q_heads * std::max(2.f, cuts) * (float)a.c.D * 8.f / kJoinBytes;

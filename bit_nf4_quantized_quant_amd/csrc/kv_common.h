@@ -25,12 +25,12 @@ struct Partial {
   float2* stat;  // [rows][splits]: reference, sum
 };
 
-// What a kernel's workgroups cost, in microseconds: to start and finish, and per
-// position that one walks through, alone on its CU or (`shared`) beside a second one.
+// What a kernel's workgroup costs alone on its CU, in microseconds: to start and
+// finish, and a position.
 struct Cost {
   int tile_rows;
   int per_cu;              // workgroups that fit a CU
-  float base, position, shared;
+  float base, position;
 };
 
 // The split with the smallest estimated time, which goes to *us.

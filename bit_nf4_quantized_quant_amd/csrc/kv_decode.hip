@@ -473,8 +473,7 @@ hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Pa
 }  // namespace
 
 // Measured with eight sequences of 1000 positions: 6 us and, a position, 6.2 and 10.5 ns at
-// D = 64 and 128 with 32 rows, 5.0, 7.4 and 15.2 ns at D = 64, 128, 256 with 16; two
-// workgroups on a CU slow each other by about 1.5.  So 40 rows on each of 32 pairs of
+// D = 64 and 128 with 32 rows, 5.0, 7.4 and 15.2 ns at D = 64, 128, 256 with 16.  So 40 rows on each of 32 pairs of
 // sequence and head, 1024 positions of 64, take 12.8 us in tiles of 32 and 9.8 us in tiles
 // of 16, but 64 rows on 128 pairs, 1000 positions of 128, 18.0 us and 20.2 us.  At D = 256
 // the registers hold 16 rows only (five queries of eight heads on 32 pairs, 4000 positions:
@@ -482,7 +481,7 @@ hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Pa
 Cost decode_cost(const AttnArgs& a, int rows) {
   const float ns = a.c.D == 256 ? 15.2f : a.c.D == 128 ? (rows == 16 ? 7.4f : 10.5f) : rows == 16 ? 5.0f : 6.2f;
   const int per_cu = a.c.D == 64 || (a.c.D == 128 && rows == 16) ? 2 : 1;
-  return Cost{rows, per_cu, 6.f, 1e-3f * ns, 1e-3f * ns * (per_cu == 2 ? 1.5f : 1.f)};
+  return Cost{rows, per_cu, 6.f, 1e-3f * ns};
 }
 
 hipError_t launch_decode(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s) {

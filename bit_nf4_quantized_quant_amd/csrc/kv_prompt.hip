@@ -519,12 +519,13 @@ hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Pa
 
 }  // namespace
 
-// One workgroup fills a CU.  Measured with eight sequences of 256 rows on 4 heads and 1000
-// positions: 5 us and, a position, 23, 35 and 78 ns at D = 64, 128, 256 (2.2 to 2.9 us a
-// tile of 8192 / D).
+// One workgroup fills a CU.  Measured with eight prompts of 16 .. 2000 tokens on 8 heads: 45,
+// 68 and 141 us at D = 64, 128, 256, the launch's 3 us among them, of which the longest
+// workgroup starts for 5 and takes 20, 31 and 67 ns a position (2.1 to 2.6 us a tile of
+// 8192 / D).
 Cost prompt_cost(const AttnArgs& a) {
-  const float us = a.c.D == 64 ? 0.023f : a.c.D == 128 ? 0.035f : 0.078f;
-  return Cost{kRows, 1, 5.f, us, us};
+  const float us = a.c.D == 64 ? 0.020f : a.c.D == 128 ? 0.031f : 0.067f;
+  return Cost{kRows, 1, 5.f, us};
 }
 
 hipError_t launch_prompt(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s) {

@@ -65,24 +65,29 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, causal: bo
     spread = np.zeros((n, hq, d))
     lse = np.full((n, hq), -np.inf)
     size = np.zeros((n, hq))
-    j = np.arange(length)
-    for i in range(n):
-        p = length - n + i
-        seen = np.ones(length, bool) if absent is None else ~absent
-        if causal:
-            seen &= j <= p
-        if window > 0:
-            seen &= j > p - window
-        if not seen.any():
-            continue
-        for h in range(hq):
-            ks, vs = k[seen, h // (hq // hkv)], v[seen, h // (hq // hkv)]
-            s = ks @ q[i, h] * scale
-            m = s.max()
+    j, p = np.arange(length), length - n + np.arange(n)[:, None]
+    seen = np.ones((n, length), bool) if absent is None else np.repeat(~absent[None], n, 0)
+    if causal:
+        seen &= j <= p
+    if window > 0:
+        seen &= j > p - window
+    # queries that see a position which is not finite: by themselves, over what they see alone
+    odd = ~(np.isfinite(k).all((1, 2)) & np.isfinite(v).all((1, 2)))
+    alone = seen[:, odd].any(1)
+    kf, vf = np.where(odd[:, None, None], 0.0, k), np.where(odd[:, None, None], 0.0, v)
+    for h in range(hq):
+        for rows, keys in [(np.flatnonzero(seen.any(1) & ~alone), slice(None))] + \
+                [(np.array([i]), seen[i]) for i in np.flatnonzero(alone)]:
+            if not len(rows):
+                continue
+            ks, vs = ((x if alone[rows[0]] else y)[keys, h // (hq // hkv)] for x, y in ((k, kf), (v, vf)))
+            there = seen[rows][:, keys]
+            s = np.where(there, q[rows, h] @ ks.T * scale, -np.inf)
+            m = s.max(1, keepdims=True)
             w = np.exp(s - m)
-            t = w.sum()
-            out[i, h] = w @ vs / t
-            spread[i, h] = w @ np.abs(vs) / t
-            lse[i, h] = m + np.log(t)
-            size[i, h] = np.max(np.abs(ks) @ np.abs(q[i, h])) * abs(scale)
+            t = w.sum(1, keepdims=True)
+            out[rows, h] = w @ vs / t
+            spread[rows, h] = w @ np.abs(vs) / t
+            lse[rows, h] = (m + np.log(t))[:, 0]
+            size[rows, h] = np.where(there, np.abs(q[rows, h]) @ np.abs(ks).T * abs(scale), 0.0).max(1)
     return out, lse, spread, size

@@ -109,6 +109,10 @@ def test_store_and_read_back_are_exact(table, T, H, D, page, f32):
                 assert np.array_equal(bf16_f64(host_bf16_bits(back)), bf16_f64(kv_oracle.bf16_bits(ref))), name
 
 
+def test_many_bf16_tokens_are_exact():
+    test_store_and_read_back_are_exact(0, 1031, 40, 128, 64, False)
+
+
 @pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
 def test_a_run_with_a_non_finite_element_reads_back_as_nan(bad):
     x = np.random.default_rng(1).normal(0, 1, (3, 2, 128)).astype(np.float32)
@@ -311,6 +315,70 @@ def test_one_large_position(D, n):
     for at in (0, 5, 19, 37, 50, 77, 101, 140):
         run_case(1050 + at, [150], [n], 1, 1, D, 16, 0, causal=False, spike=(at, 2.0 ** 18),
                  scale=D ** -0.5 * 2.0 ** -18)
+
+
+# ------------------------------------------------------------------ batches that fill the device
+
+# The kernel is chosen by its estimated time: on an MI355X's 256 CUs these batches are large
+# enough for tiles of 32, and of 256, query rows.  (kv heads, lengths, queries)
+LARGE = {32: (32, [333, 77, 5, 40], [40, 33, 1, 40]), 256: (48, [333, 77, 3, 60], [130, 77, 3, 40])}
+LARGE_KERNELS = [(64, 32), (128, 32), (64, 256), (128, 256), (256, 256)]
+
+
+@pytest.mark.parametrize("D,rows", LARGE_KERNELS)
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 33), (False, 100), (True, 1)])
+def test_large_batches(D, rows, causal, window):
+    heads, lengths, queries = LARGE[rows]
+    run_case(1300 + D + rows, lengths, queries, heads, 1, D, 16 if causal else 48, D // 64 % 3, causal=causal,
+             window=window, strided=window == 33)
+
+
+@pytest.mark.parametrize("D,Hkv,G,n", [(64, 20, 3, 100), (64, 10, 7, 90), (128, 16, 3, 90), (128, 12, 8, 40),
+                                       (256, 8, 5, 110), (256, 3, 32, 30)])
+def test_large_batches_on_shared_heads(D, Hkv, G, n):
+    run_case(1320 + D + G, [310, 64, 1, 0, n], [n, 64, 1, 2, n - 5], Hkv, G, D, 32, 0)
+
+
+@pytest.mark.parametrize("D,rows", LARGE_KERNELS)
+def test_large_batches_without_some_pages(D, rows):
+    heads, lengths, queries = LARGE[rows]
+    run_case(1340 + D + rows, lengths, queries, heads, 1, D, 16, 0, hide=(0, 2))
+    run_case(1341 + D + rows, lengths, queries, heads, 1, D, 128, 0, hide=(1, 0), window=60)
+
+
+@pytest.mark.parametrize("D,rows", LARGE_KERNELS)
+def test_large_batches_with_non_finite_positions(D, rows):
+    heads, _, queries = LARGE[rows]
+    n = queries[0]
+    out = run_case(1360 + D + rows, [300, 300, 150], [n, n, 40], heads, 1, D, 32, 0, spoil=(0, [297, 298]))
+    assert np.isfinite(out[:n - 3]).all() and np.isnan(out[n - 3:n]).all() and np.isfinite(out[n:]).all()
+
+
+@pytest.mark.parametrize("D,rows", LARGE_KERNELS)
+@pytest.mark.parametrize("gain", [2.0 ** -90, 2.0 ** 60])
+def test_large_batches_magnitudes(D, rows, gain):
+    heads, lengths, queries = LARGE[rows]
+    run_case(1380 + D + rows, lengths, queries, heads, 1, D, 16, 0, gain=gain, scale=D ** -0.5 / gain)
+
+
+@pytest.mark.parametrize("D,rows", LARGE_KERNELS)
+@pytest.mark.parametrize("at", [0, 19, 37, 77, 140])
+def test_large_batches_one_large_position(D, rows, at):
+    heads, _, queries = LARGE[rows]
+    n = queries[0]
+    run_case(1400 + at + rows, [150, 140, 60], [n, n, 40], heads, 1, D, 16, 0, causal=False, spike=(at, 2.0 ** 18),
+             scale=D ** -0.5 * 2.0 ** -18)
+
+
+@pytest.mark.parametrize("D,Hkv,n", [(64, 16, 513), (128, 16, 260), (256, 8, 260)])
+@pytest.mark.parametrize("window", [0, 700])
+def test_prompts_with_their_positions_split(D, Hkv, n, window):
+    """The first sequence's rows have several splits to join, some of the second's one, the last's none."""
+    run_case(1440 + D, [1500, 700, 0], [n, n - 30, 1], Hkv, 1, D, 64, 0, window=window)
+
+
+def test_wide_heads_with_many_splits():
+    run_case(1460, [6000, 2500], [1, 1], 2, 3, 256, 64, 0, uniform=True)
 
 
 def test_strides_and_other_streams():
