@@ -131,11 +131,10 @@ __device__ __forceinline__ uint32_t v_at(int pos, int chunk) {
 
 template <int D, int kNQ>
 struct Smem {
-  static constexpr int kPitch = 68;             // floats per row of the joining passes (64 + padding)
-  static constexpr size_t kJoin = (size_t)kWaves * 16 * kPitch * 4;
-  static constexpr size_t kStats = (size_t)kWaves * 16 * kNQ * 2 * 4;
-  static constexpr size_t kBytes = kPairBytes + kStats;
-  static_assert(kJoin <= kPairBytes, "the joining passes fit over the pair table");
+  static constexpr int kPitch = D + 4;          // floats per row of the join (with padding)
+  static constexpr size_t kJoin = (size_t)kWaves * 16 * kPitch * 4;   // over the pair table
+  static constexpr size_t kStatsOff = kJoin > kPairBytes ? kJoin : kPairBytes;
+  static constexpr size_t kBytes = kStatsOff + (size_t)kWaves * 16 * kNQ * 2 * 4;
 };
 
 template <int D, int kNQ>
@@ -402,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
 
   // ---- join the eight waves
   __syncthreads();                              // (the pair table is done with)
-  float2* stats = reinterpret_cast<float2*>(smem + kPairBytes);
+  float2* stats = reinterpret_cast<float2*>(smem + Smem<D, kNQ>::kStatsOff);
 #pragma unroll
   for (int j = 0; j < kNQ; ++j) {
     l[j] = rows_add(l[j]);
@@ -431,20 +430,20 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
     const int i = div_by(r, a.group_div);
     const int64_t out_row = (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
     const float inv = rsum == 0.f ? 0.f : lv.inv_kappa / rsum;
+    if (j > 0) __syncthreads();                 // (the rows before have been summed)
+#pragma unroll
+    for (int c = 0; c < 4 * NB; ++c) {
+      f32x4 v = o[j][c];
+      v *= f;
+      *reinterpret_cast<f32x4*>(buf + (wave * 16 + col) * P + 16 * c + 4 * quad) = v;
+    }
+    __syncthreads();
 #pragma unroll
     for (int e = 0; e < NB; ++e) {
-      __syncthreads();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        f32x4 v = o[j][4 * e + c];
-        v *= f;
-        *reinterpret_cast<f32x4*>(buf + (wave * 16 + col) * P + 16 * c + 4 * quad) = v;
-      }
-      __syncthreads();
       float2 s = make_float2(0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        const float2 v = *reinterpret_cast<const float2*>(buf + (w * 16 + orow) * P + 2 * (tid & 31));
+        const float2 v = *reinterpret_cast<const float2*>(buf + (w * 16 + orow) * P + e * 64 + 2 * (tid & 31));
         s.x += v.x, s.y += v.y;
       }
       if (r < rows) {
