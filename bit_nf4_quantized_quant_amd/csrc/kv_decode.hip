@@ -15,13 +15,13 @@
 // the joining, 285 MB at 4.5 TB/s (the kernel alone 58 us; in its middle it reads
 // 7 TB/s, the rest is the start and the joins); 32 sequences of 1 .. 4096
 // positions 30 us (2.5 TB/s: the longest sequences' workgroups walk twice the
-// mean); one sequence of 700, 32 heads 10.7 us.
+// mean); one sequence of 700, 32 heads 10.6 us.
 //
 // Split.  A workgroup takes one kv head, 16 kNQ query rows and a chunk of the
 // positions; its eight waves take tiles of 32 positions in turn, each with its
 // own running maximum and sum, and join over LDS at the end.  Where one chunk
 // does not cover the sequence the workgroups leave (maximum, sum, weighted
-// values) in the workspace and kv_join_kernel joins them.
+// values) in the workspace for the joining kernels.
 //
 // A tile in a wave.  Scores come out transposed, S^T = K Q^T by 16x16x32
 // products (rows are positions, columns are queries), so that a lane holds one
