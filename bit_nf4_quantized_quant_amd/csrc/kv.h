@@ -77,15 +77,23 @@ struct AttnArgs {
 hipError_t launch_kv_write(const WriteArgs& a, hipStream_t s);
 hipError_t launch_kv_read(const ReadArgs& a, hipStream_t s);
 
-// How the positions of a row tile are cut.
+// How the work on some sequences is cut: the query rows of a head into row tiles, the
+// positions that a tile sees into splits.
 struct Split {
   int chunk, splits;           // positions per split, splits
   int rows, tiles, tile_rows;  // query rows of a head at most, row tiles, rows of one
+  int above, upto;             // the sequences: those of more than `above` and at most `upto` query rows
+  int listed;                  // 0: a grid of tiles and sequences; or a bound of the sequences' tiles, taken one after the other
+  int part_q;                  // 0: a row's partial results lie at its token; or room for so many queries a sequence
 };
-// Which kernel an attention call takes, its split, and the workspace it needs.
-struct AttnPlan {
+// Which kernels an attention call takes, and the workspace it needs.
+struct AttnPass {
   bool prompt;
   Split split;
+};
+struct AttnPlan {
+  AttnPass pass[2];
+  int passes;
   size_t workspace;
 };
 AttnPlan kv_attention_plan(const AttnArgs& a);

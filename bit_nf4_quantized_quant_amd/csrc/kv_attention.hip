@@ -2,6 +2,7 @@
 // few and for many query rows, the split of the positions, and the kernel that
 // joins the splits.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "kv_common.h"
@@ -22,14 +23,29 @@ namespace {
 // a row, 3.9 us so).
 constexpr int kJoinRows = 16;
 
+// The workgroup's rows: blockIdx.x counts pieces of `step` rows, of all tiles of a head.
+__device__ __forceinline__ bool join_place(const AttnArgs& a, const Split& sp, int step, int& b, int& head, int& first) {
+  const int per = sp.tile_rows / step, pieces = sp.listed ? sp.listed * per : (sp.rows + step - 1) / step;
+  const int piece = blockIdx.x % pieces;
+  head = blockIdx.x / pieces;
+  b = blockIdx.y;
+  first = piece * step;
+  if (!sp.listed) return true;
+  int tile;
+  if (!listed_tile(a, sp, piece / per, b, tile)) return false;
+  first = tile * sp.tile_rows + piece % per * step;
+  return true;
+}
+
 template <int D>
 __global__ void __launch_bounds__(256) kv_join_rows_kernel(AttnArgs a, Split sp, float inv_kappa, Partial part) {
   constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
-  const int group = (int)a.group_div.d, blocks = (sp.rows + kJoinRows - 1) / kJoinRows;
-  const int first = blockIdx.x % blocks * kJoinRows, head = blockIdx.x / blocks, b = blockIdx.y;
+  const int group = (int)a.group_div.d;
+  int b, head, first;
+  if (!join_place(a, sp, kJoinRows, b, head, first)) return;
   const Seq seq = sequence(a, b);
   const int rows = seq.n * group;
-  if (first >= rows) return;
+  if (first >= rows || !taken(sp, rows)) return;
   const int r0 = first / sp.tile_rows * sp.tile_rows;
   const Span span = tile_span(a, seq, div_by(r0, a.group_div), div_by(min(r0 + sp.tile_rows, rows) - 1, a.group_div));
   const int live = live_splits(span, sp.chunk, sp.splits);
@@ -38,8 +54,9 @@ __global__ void __launch_bounds__(256) kv_join_rows_kernel(AttnArgs a, Split sp,
   for (int r = first + threadIdx.x / kLanes; r < min(first + kJoinRows, rows); r += kGroups) {
     const int i = div_by(r, a.group_div);
     const int64_t row = (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
-    const float2* stat = part.stat + row * sp.splits;
-    const f32x4* o = reinterpret_cast<const f32x4*>(part.o + row * sp.splits * D) + col;
+    const int64_t from = partial_row(a, sp, seq, b, i, head * group + (r - i * group)) * sp.splits;
+    const float2* stat = part.stat + from;
+    const f32x4* o = reinterpret_cast<const f32x4*>(part.o + from * D) + col;
     float top = -INFINITY, sum = 0.f;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     for (int s = 0; s < live; ++s) top = fmaxf(top, stat[s].x);
@@ -70,18 +87,20 @@ __global__ void __launch_bounds__(256) kv_join_splits_kernel(AttnArgs a, Split s
   __shared__ float wave_top[4], wave_sum[4];
   __shared__ f32x4 acc[256];
   const int group = (int)a.group_div.d;
-  const int r = blockIdx.x % sp.rows, head = blockIdx.x / sp.rows, b = blockIdx.y;
+  int b, head, r;
+  if (!join_place(a, sp, 1, b, head, r)) return;
   const Seq seq = sequence(a, b);
   const int rows = seq.n * group;
-  if (r >= rows) return;
+  if (r >= rows || !taken(sp, rows)) return;
   const int r0 = r / sp.tile_rows * sp.tile_rows;
   const Span span = tile_span(a, seq, div_by(r0, a.group_div), div_by(min(r0 + sp.tile_rows, rows) - 1, a.group_div));
   const int splits = live_splits(span, sp.chunk, sp.splits);
   if (splits == 1) return;
   const int i = div_by(r, a.group_div);
   const int64_t row = (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
-  const float2* stat = part.stat + row * sp.splits;
-  const f32x4* o = reinterpret_cast<const f32x4*>(part.o + row * sp.splits * D);
+  const int64_t from = partial_row(a, sp, seq, b, i, head * group + (r - i * group)) * sp.splits;
+  const float2* stat = part.stat + from;
+  const f32x4* o = reinterpret_cast<const f32x4*>(part.o + from * D);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   // the common reference
   float top = -INFINITY;
@@ -131,8 +150,9 @@ constexpr int kManySplits = 8;   // from here on a row has enough splits for a w
 
 template <int D>
 hipError_t launch_join(const AttnArgs& a, const Split& sp, float inv_kappa, const Partial& part, hipStream_t s) {
-  const int64_t rows = sp.splits < kManySplits ? (sp.rows + kJoinRows - 1) / kJoinRows : sp.rows;
-  const dim3 grid((unsigned)(rows * a.c.heads), (unsigned)a.seqs);
+  const int step = sp.splits < kManySplits ? kJoinRows : 1;
+  const int64_t pieces = sp.listed ? (int64_t)sp.listed * (sp.tile_rows / step) : (sp.rows + step - 1) / step;
+  const dim3 grid((unsigned)(pieces * a.c.heads), (unsigned)(sp.listed ? 1 : a.seqs));
   const auto kernel = sp.splits < kManySplits ? kv_join_rows_kernel<D> : kv_join_splits_kernel<D>;
   hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, sp, inv_kappa, part);
   return hipGetLastError();
@@ -179,7 +199,7 @@ Split split_of(const AttnArgs& a, const Cost& cost, float* us) {
     }
     if (t < *us) {
       *us = t;
-      best = Split{(int)chunk, (int)splits, (int)rows, (int)tiles, cost.tile_rows};
+      best = Split{(int)chunk, (int)splits, (int)rows, (int)tiles, cost.tile_rows, 0, INT_MAX, 0, 0};
     }
     if (chunk == 256) break;
   }
@@ -191,26 +211,60 @@ Split split_of(const AttnArgs& a, const Cost& cost, float* us) {
 // choice is by the estimated times: 256 rows on each of 32 heads and 1000 positions, D =
 // 128, take 19 us with the first and 40 us with the second (as 32 workgroups do not fill
 // the device); 128 rows on 128 heads and 300 positions 25 us and 16.5 us.
-AttnPlan kv_attention_plan(const AttnArgs& a) {
+static AttnPass best_pass(const AttnArgs& a) {
   float least = 0.f, us = 0.f;
-  AttnPlan plan{false, split_of(a, decode_cost(a, 16), &least), 0};
-  if (a.c.D < 256 && plan.split.rows > 16) {
+  AttnPass pass{false, split_of(a, decode_cost(a, 16), &least)};
+  if (a.c.D < 256 && pass.split.rows > 16) {
     const Split s = split_of(a, decode_cost(a, 32), &us);
-    if (us < least) plan.split = s, least = us;
+    if (us < least) pass.split = s, least = us;
   }
   const Split s = split_of(a, prompt_cost(a), &us);
-  if (us < least) plan.split = s, plan.prompt = true;
-  if (plan.split.splits > 1)
-    plan.workspace = (size_t)(a.tokens * a.q_heads) * plan.split.splits * (a.c.D * sizeof(float) + sizeof(float2));
+  if (us < least) pass.split = s, pass.prompt = true;
+  return pass;
+}
+
+// Prompts and single steps in one batch, which few tokens for seqs and max_q tell, take two
+// passes: one for the sequences of more than kStepRows query rows (and more than a query),
+// its tiles listed, as most of a grid of tiles and sequences would be empty, and one for
+// the others.  A prompt of 2048 and 63 steps on 4096 positions, 32 heads on 8 of 128: 591 us
+// in one pass, 237 us in two; a prompt of 8192 and 255 steps on 1000: 2618 and 774 us.
+AttnPlan kv_attention_plan(const AttnArgs& a) {
+  constexpr int64_t kStepRows = 32;
+  const int64_t group = a.q_heads / a.c.heads, step_q = std::max<int64_t>(1, kStepRows / group);
+  auto workspace = [&](const Split& sp) {
+    const int64_t tokens = sp.part_q ? a.seqs * sp.part_q : a.tokens;
+    return sp.splits == 1 ? 0 : (size_t)(tokens * a.q_heads) * sp.splits * (a.c.D * sizeof(float) + sizeof(float2));
+  };
+  AttnPlan plan{};
+  if (a.max_q <= step_q || 4 * a.tokens > a.seqs * a.max_q) {
+    plan.passes = 1;
+    plan.pass[0] = best_pass(a);
+  } else {
+    plan.passes = 2;
+    const int border = (int)(step_q * group);
+    AttnArgs prompts = a, steps = a;
+    prompts.seqs = (a.tokens + a.max_q - 1) / a.max_q;          // (at least; for the estimate)
+    plan.pass[0] = best_pass(prompts);
+    Split& first = plan.pass[0].split;
+    first.above = border;
+    const int64_t most = std::min<int64_t>(a.seqs, a.tokens / (step_q + 1));
+    first.listed = (int)std::max<int64_t>(1, a.tokens * group / first.tile_rows + most);
+    steps.max_q = step_q;
+    steps.tokens = std::min(a.tokens, a.seqs);                  // (mostly a query each)
+    plan.pass[1] = best_pass(steps);
+    plan.pass[1].split.upto = border;
+    plan.pass[1].split.part_q = (int)step_q;
+  }
+  for (int i = 0; i < plan.passes; ++i) plan.workspace = std::max(plan.workspace, workspace(plan.pass[i].split));
   return plan;
 }
 
-hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
-  const Split& sp = plan.split;
+static hipError_t launch_pass(const AttnArgs& a, const AttnPass& pass, hipStream_t s) {
+  const Split& sp = pass.split;
   Partial part;
   part.o = static_cast<float*>(a.workspace);
-  part.stat = reinterpret_cast<float2*>(part.o + (size_t)(a.tokens * a.q_heads) * sp.splits * a.c.D);
-  const hipError_t e = plan.prompt ? launch_prompt(a, sp, part, s) : launch_decode(a, sp, part, s);
+  part.stat = reinterpret_cast<float2*>(part.o + (size_t)((sp.part_q ? a.seqs * sp.part_q : a.tokens) * a.q_heads) * sp.splits * a.c.D);
+  const hipError_t e = pass.prompt ? launch_prompt(a, sp, part, s) : launch_decode(a, sp, part, s);
   if (e != hipSuccess || sp.splits == 1) return e;
   const float inv_kappa = fp16_levels(a.c.table).inv_kappa;
   switch (a.c.D) {
@@ -218,6 +272,14 @@ hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& plan, hipStrea
     case 128: return launch_join<128>(a, sp, inv_kappa, part, s);
     default: return launch_join<256>(a, sp, inv_kappa, part, s);
   }
+}
+
+hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
+  for (int i = 0; i < plan.passes; ++i) {       // (in turn: they share the workspace)
+    const hipError_t e = launch_pass(a, plan.pass[i], s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace kv

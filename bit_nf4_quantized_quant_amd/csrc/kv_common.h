@@ -51,20 +51,56 @@ struct Seq {
   int64_t shift;   // query i stands at position shift + i
 };
 
+__device__ __forceinline__ void queries(const AttnArgs& a, int b, int& q0, int& n) {
+  if (a.q_starts) {
+    const int tokens = (int)a.tokens;
+    q0 = min(max(a.q_starts[b], 0), tokens);
+    n = min(min(max(a.q_starts[b + 1] - q0, 0), (int)a.max_q), tokens - q0);
+  } else {
+    q0 = b * (int)a.max_q;
+    n = (int)a.max_q;
+  }
+}
 __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
   Seq s;
   const int length = a.lengths[b];
-  if (a.q_starts) {
-    const int tokens = (int)a.tokens;
-    s.q0 = min(max(a.q_starts[b], 0), tokens);
-    s.n = min(min(max(a.q_starts[b + 1] - s.q0, 0), (int)a.max_q), tokens - s.q0);
-  } else {
-    s.q0 = b * (int)a.max_q;
-    s.n = (int)a.max_q;
-  }
+  queries(a, b, s.q0, s.n);
   s.len = min(max(length, 0), (int)a.table_width * (int)a.c.page_size);
   s.shift = (int64_t)length - s.n;
   return s;
+}
+
+// Whether a pass is for a sequence of so many query rows.
+__device__ __forceinline__ bool taken(const Split& sp, int rows) { return rows > sp.above && rows <= sp.upto; }
+
+// The sequence and the row tile of a pass's slot-th tile, by a wave: false if it has fewer.
+__device__ __forceinline__ bool listed_tile(const AttnArgs& a, const Split& sp, int slot, int& b, int& tile) {
+  const int lane = threadIdx.x & 63, group = (int)a.group_div.d;
+  for (int b0 = 0; b0 < (int)a.seqs; b0 += 64) {
+    int q0 = 0, n = 0;
+    if (b0 + lane < (int)a.seqs) queries(a, b0 + lane, q0, n);
+    const int tiles = taken(sp, n * group) ? (n * group + sp.tile_rows - 1) / sp.tile_rows : 0;
+    int sum = tiles;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) {
+      const int below = __shfl_up(sum, x);
+      if (lane >= x) sum += below;
+    }
+    const uint64_t past = __ballot(sum > slot);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      b = b0 + at;
+      tile = slot - (__builtin_amdgcn_readlane(sum, at) - __builtin_amdgcn_readlane(tiles, at));
+      return true;
+    }
+    slot -= __builtin_amdgcn_readlane(sum, 63);
+  }
+  return false;
+}
+
+// Where the partial results of query i of a sequence, query head h, lie.
+__device__ __forceinline__ int64_t partial_row(const AttnArgs& a, const Split& sp, const Seq& s, int b, int i, int h) {
+  return (int64_t)((sp.part_q ? b * sp.part_q : s.q0) + i) * a.q_heads + h;
 }
 
 // Positions [low, high) that query i sees.

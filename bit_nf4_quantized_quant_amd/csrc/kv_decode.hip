@@ -146,11 +146,14 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
   char* lut = smem;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, quad = lane >> 4;
+  const int count = sp.listed ? sp.listed : sp.tiles, slot = blockIdx.x / sp.splits % count;
+  const int head = blockIdx.x / sp.splits / count, group = (int)a.group_div.d;
+  int b = blockIdx.y, tile = slot;
+  if (sp.listed && !listed_tile(a, sp, slot, b, tile)) return;
+  const int r0 = tile * kRows;
   // (neighbours go to different XCDs: with the split turned by the sequence none gets
   // only the last splits, which short sequences do not have)
-  const int b = blockIdx.y, split = (blockIdx.x + b) % sp.splits;
-  const int head = blockIdx.x / sp.splits / sp.tiles, r0 = blockIdx.x / sp.splits % sp.tiles * kRows;
-  const int group = (int)a.group_div.d;
+  const int split = (blockIdx.x + (sp.listed ? slot : b)) % sp.splits;
   // the first pages are fetched, and the pair table is made, while the sequence's numbers
   // are on their way: without a window the positions start at 0
   const int32_t* table = a.block_table + (int64_t)b * a.table_width;
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
   build_pairs<kThreads>(lv, lut);
   const Seq seq = sequence(a, b);
   const int rows = seq.n * group;
-  if (r0 >= rows) return;
+  if (r0 >= rows || !taken(sp, rows)) return;
   const int i_first = div_by(r0, a.group_div), i_last = div_by(min(r0 + kRows, rows) - 1, a.group_div);
   const Span span = tile_span(a, seq, i_first, i_last);
   const int live = live_splits(span, sp.chunk, sp.splits);
@@ -429,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
     }
     const int i = div_by(r, a.group_div);
     const int64_t out_row = (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
+    auto part_row = [&]() { return partial_row(a, sp, seq, b, i, head * group + (r - i * group)) * sp.splits + split; };
     const float inv = rsum == 0.f ? 0.f : lv.inv_kappa / rsum;
     if (j > 0) __syncthreads();                 // (the rows before have been summed)
 #pragma unroll
@@ -450,12 +454,12 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
         if (live == 1)
           reinterpret_cast<uint32_t*>(a.out + out_row * D + e * 64)[tid & 31] = pack_bf16x2(s.x * inv, s.y * inv);
         else
-          reinterpret_cast<float2*>(part.o + (out_row * sp.splits + split) * D + e * 64)[tid & 31] = s;
+          reinterpret_cast<float2*>(part.o + part_row() * D + e * 64)[tid & 31] = s;
       }
     }
     if (r < rows && (tid & 31) == 0) {
       if (live > 1)
-        part.stat[out_row * sp.splits + split] = make_float2(rtop, rsum);
+        part.stat[part_row()] = make_float2(rtop, rsum);
       else if (a.lse)
         a.lse[out_row] = rsum == 0.f ? -INFINITY : kLn2 * (rtop + __builtin_amdgcn_logf(rsum));
     }
@@ -464,8 +468,9 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
 
 template <int D, int kNQ>
 hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Partial& part, hipStream_t s) {
-  hipLaunchKernelGGL((kv_decode_kernel<D, kNQ>), dim3((unsigned)(sp.splits * sp.tiles * a.c.heads), (unsigned)a.seqs),
-                     dim3(kThreads), 0, s, a, sp, lv, part);
+  const dim3 grid((unsigned)(sp.splits * (sp.listed ? sp.listed : sp.tiles) * a.c.heads),
+                  (unsigned)(sp.listed ? 1 : a.seqs));
+  hipLaunchKernelGGL((kv_decode_kernel<D, kNQ>), grid, dim3(kThreads), 0, s, a, sp, lv, part);
   return hipGetLastError();
 }
 

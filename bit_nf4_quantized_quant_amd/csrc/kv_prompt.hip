@@ -130,8 +130,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
   // the last row tiles of a sequence see most: those of all sequences start first
-  const int rest = blockIdx.x / sp.splits, b = blockIdx.y;
-  const int head = rest % (int)a.c.heads, tile = rest / (int)a.c.heads * (int)gridDim.z + blockIdx.z;
+  const int rest = blockIdx.x / sp.splits, head = rest % (int)a.c.heads;
+  const int slot = rest / (int)a.c.heads * (int)gridDim.z + blockIdx.z;
+  int b = blockIdx.y, tile = slot;
+  if (sp.listed && !listed_tile(a, sp, slot, b, tile)) return;
   // (neighbours go to different XCDs: with the split turned by the tile none gets only
   // the last splits, which most tiles do not have)
   const int split = (blockIdx.x + blockIdx.z) % sp.splits;
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const Seq seq = sequence(a, b);
   const int rows = seq.n * group;
   const int r0 = ((rows + kRows - 1) / kRows - 1 - tile) * kRows;
-  if (r0 < 0) return;
+  if (r0 < 0 || !taken(sp, rows)) return;
   const Span span = tile_span(a, seq, div_by(r0, a.group_div), div_by(min(r0 + kRows, rows) - 1, a.group_div));
   const int live = live_splits(span, sp.chunk, sp.splits);
   if (split >= live) return;
@@ -462,9 +464,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   int me = lane;
   asm volatile("" : "+v"(me));                  // what follows is not worth registers during the loop
   const int my_row = me & 31, my_half = me >> 5;
-  auto row_of = [&](int r) -> int64_t {         // of the output and of the statistics
-    const int i = div_by(r, a.group_div);
-    return (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
+  auto row_of = [&](int r) -> int64_t {         // of the output, or of the partial results
+    const int i = div_by(r, a.group_div), h = head * group + (r - i * group);
+    return live > 1 ? partial_row(a, sp, seq, b, i, h) : (int64_t)(seq.q0 + i) * a.q_heads + h;
   };
   if (live > 1) {
     constexpr int kPart = D == 64 ? 64 : 128, kChunks = kPart / 4, kStore = 64 / kChunks;   // elements a pass
@@ -511,8 +513,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 template <int D>
 hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Partial& part, hipStream_t s) {
-  const int z = std::min(sp.tiles, 32768);      // (a grid's y and z end at 65535)
-  const dim3 grid((unsigned)(sp.splits * a.c.heads * ((sp.tiles + z - 1) / z)), (unsigned)a.seqs, (unsigned)z);
+  const int count = sp.listed ? sp.listed : sp.tiles, z = std::min(count, 32768);   // (a grid's y and z end at 65535)
+  const dim3 grid((unsigned)(sp.splits * a.c.heads * ((count + z - 1) / z)), (unsigned)(sp.listed ? 1 : a.seqs), (unsigned)z);
   hipLaunchKernelGGL(kv_prompt_kernel<D>, grid, dim3(kThreads), 0, s, a, sp, lv, part);
   return hipGetLastError();
 }

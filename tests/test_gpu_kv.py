@@ -377,6 +377,22 @@ def test_prompts_with_their_positions_split(D, Hkv, n, window):
     run_case(1440 + D, [1500, 700, 0], [n, n - 30, 1], Hkv, 1, D, 64, 0, window=window)
 
 
+@pytest.mark.parametrize("D,Hkv,G", [(64, 2, 4), (64, 24, 2), (128, 2, 1), (128, 1, 40), (128, 48, 1), (256, 2, 3)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 50)])
+def test_prompts_and_steps_in_one_batch(D, Hkv, G, causal, window):
+    """Few tokens for the sequences and the longest one's queries: two passes, whose border is at 32 query rows."""
+    step = max(1, 32 // G)
+    queries = [130, 1, step, step + 1, 0, 2, 1] + [1] * 9 + [40]
+    lengths = [max(n, x) for n, x in zip(queries, [333, 1, 77, 64, 5, 0, 100] + [17 * i for i in range(9)] + [200])]
+    run_case(1480 + D + G, lengths, queries, Hkv, G, D, 16, 0, causal=causal, window=window, hide=(0, 3))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prompts_and_steps_with_their_positions_split(D):
+    run_case(1500 + D, [3000, 5000, 40, 1, 2600, 0, 0, 0, 300], [280, 1, 3, 1, 1, 0, 0, 0, 9], 4, 2, D, 64, 0)
+    run_case(1510 + D, [100] * 70 + [400, 900] + [30] * 5, [1] * 70 + [300, 200] + [3] * 5, 1, 4, D, 16, 0)
+
+
 def test_wide_heads_with_many_splits():
     run_case(1460, [6000, 2500], [1, 1], 2, 3, 256, 64, 0, uniform=True)
 
