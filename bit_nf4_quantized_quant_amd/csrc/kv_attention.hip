@@ -209,8 +209,8 @@ Split split_of(const AttnArgs& a, const Cost& cost, float* us) {
 // The kernel for few rows shares a tile's expanded codes between 16 or 32 query rows, that
 // for many between 256, but its workgroup takes as long for one row as for 256.  So the
 // choice is by the estimated times: 256 rows on each of 32 heads and 1000 positions, D =
-// 128, take 19 us with the first and 40 us with the second (as 32 workgroups do not fill
-// the device); 128 rows on 128 heads and 300 positions 25 us and 16.5 us.
+// 128, take 18 us with the first and 29 us with the second (as 32 workgroups do not fill
+// the device); 128 rows on 128 heads and 300 positions 24 us and 15.6 us.
 static AttnPass best_pass(const AttnArgs& a) {
   float least = 0.f, us = 0.f;
   AttnPass pass{false, split_of(a, decode_cost(a, 16), &least)};

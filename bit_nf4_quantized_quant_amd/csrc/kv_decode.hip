@@ -404,11 +404,14 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
 
   // ---- join the eight waves
   __syncthreads();                              // (the pair table is done with)
+  int me = tid;
+  asm volatile("" : "+v"(me));                  // what follows is not worth registers during the loop
+  const int my_col = me & 15, my_quad = me >> 4 & 3;
   float2* stats = reinterpret_cast<float2*>(smem + Smem<D, kNQ>::kStatsOff);
 #pragma unroll
   for (int j = 0; j < kNQ; ++j) {
     l[j] = rows_add(l[j]);
-    if (quad == 0) stats[(wave * kNQ + j) * 16 + col] = make_float2(m[j], l[j]);
+    if (my_quad == 0) stats[(wave * kNQ + j) * 16 + my_col] = make_float2(m[j], l[j]);
   }
   __syncthreads();
   float* buf = reinterpret_cast<float*>(smem);
@@ -417,10 +420,10 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
   for (int j = 0; j < kNQ; ++j) {
     float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stats[(w * kNQ + j) * 16 + col].x);
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stats[(w * kNQ + j) * 16 + my_col].x);
     const float f = exp2_fast(m[j] - (top == -INFINITY ? 0.f : top));
-    // the row a thread sums: row tid / 32, elements 2 (tid % 32) of each run
-    const int orow = tid >> 5, r = r0 + 16 * j + orow;
+    // the row a thread sums: row me / 32, elements 2 (me % 32) of each run
+    const int orow = me >> 5, r = r0 + 16 * j + orow;
     float rtop = -INFINITY, rsum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) rtop = fmaxf(rtop, stats[(w * kNQ + j) * 16 + orow].x);
@@ -439,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
     for (int c = 0; c < 4 * NB; ++c) {
       f32x4 v = o[j][c];
       v *= f;
-      *reinterpret_cast<f32x4*>(buf + (wave * 16 + col) * P + 16 * c + 4 * quad) = v;
+      *reinterpret_cast<f32x4*>(buf + (wave * 16 + my_col) * P + 16 * c + 4 * my_quad) = v;
     }
     __syncthreads();
 #pragma unroll
@@ -447,17 +450,17 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
       float2 s = make_float2(0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        const float2 v = *reinterpret_cast<const float2*>(buf + (w * 16 + orow) * P + e * 64 + 2 * (tid & 31));
+        const float2 v = *reinterpret_cast<const float2*>(buf + (w * 16 + orow) * P + e * 64 + 2 * (me & 31));
         s.x += v.x, s.y += v.y;
       }
       if (r < rows) {
         if (live == 1)
-          reinterpret_cast<uint32_t*>(a.out + out_row * D + e * 64)[tid & 31] = pack_bf16x2(s.x * inv, s.y * inv);
+          reinterpret_cast<uint32_t*>(a.out + out_row * D + e * 64)[me & 31] = pack_bf16x2(s.x * inv, s.y * inv);
         else
-          reinterpret_cast<float2*>(part.o + part_row() * D + e * 64)[tid & 31] = s;
+          reinterpret_cast<float2*>(part.o + part_row() * D + e * 64)[me & 31] = s;
       }
     }
-    if (r < rows && (tid & 31) == 0) {
+    if (r < rows && (me & 31) == 0) {
       if (live > 1)
         part.stat[part_row()] = make_float2(rtop, rsum);
       else if (a.lse)

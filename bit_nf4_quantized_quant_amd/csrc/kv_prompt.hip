@@ -19,7 +19,8 @@
 // the expansion; leaving any one out shortens it by no more than its own time.
 // Measured: the last 2048 tokens of 8192, 32 heads of 128: 271 us, 0.89 PFLOP/s of
 // 1.23 that a large library product reaches; six prompts of 136 .. 1500 tokens, 16 heads
-// on 4 of 256: 108 us, of which the longest workgroup's 47 tiles are 98.  Queries and
+// on 4 of 256: 99 us, of which the longest workgroup's 47 tiles are 89 (109 us with
+// queries in scratch memory, as all of a tile's addresses stayed in registers).  Queries and
 // results go through LDS to be read and written in whole rows: 16 bytes of 32 rows an
 // instruction took 4.7 and 3 to 7 us a workgroup, now 2 and 2 to 5.
 //
@@ -62,7 +63,10 @@ struct Shape {
   // values, and the tile's exponents
   static constexpr int kScaleOff = kRawOff + kWaves * 512;
   static constexpr int kScaleSize = 256 + 256 + 16;
-  static constexpr size_t kBytes = kScaleOff + 16 * kScaleSize;
+  // reduction steps whose queries wait in LDS: at D = 256 the registers do not hold all
+  static constexpr int kStored = D == 256 ? 2 : 0;
+  static constexpr int kStoredOff = kScaleOff + 16 * kScaleSize;
+  static constexpr size_t kBytes = kStoredOff + kStored * kWaves * 1024;
   static_assert(kWaves * 16384 <= kBytes, "room for the waves' turned rows");
 };
 
@@ -153,7 +157,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int w0 = r0 + 32 * wave;
   const bool active = w0 < rows;
   const int r = min(w0 + col, rows - 1), qi = div_by(r, a.group_div);
-  const int qlow = seen_low(a, seq, qi), qhigh = seen_high(a, seq, qi);
   // positions that some, and that all, of the wave's rows see
   const int i_first = div_by(min(w0, rows - 1), a.group_div), i_last = div_by(min(w0 + 32, rows) - 1, a.group_div);
   const int any_low = seen_low(a, seq, i_first), any_high = active ? seen_high(a, seq, i_last) : 0;
@@ -223,37 +226,45 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (lane == 0) *reinterpret_cast<i32x4*>(dst + 512) = i32x4{ek, ev, full, 0};
   };
-  const uint32_t lane4 = 4u * (lane & 31);
   char* raw_v = smem + S::kRawOff + wave * 512;
   // The way of a tile's share into LDS, in three steps that the products of the tile
   // before it are put between, so that none waits for the LDS round trip of the one before.
   f16x8 kx[2], vx[2], ks8, vs8[2];
   i32x2 vt;
+  // (at D = 256 lane addresses are made anew each tile: kept, they cost queries' registers)
+  auto my_lane = [&]() {
+    int l = lane;
+    if (D == 256) asm volatile("" : "+v"(l));
+    return l;
+  };
   auto stage_fetch = [&](int k) {
+    const int lane = my_lane(), half = lane >> 5;
     *reinterpret_cast<u32x2*>(raw_v + lane * 8) = v_raw;    // [chunk][position] of 16 codes each
     const _Float16 ks = reinterpret_cast<const _Float16*>(scales_of(k))[cpos * NB + (wu >> 1)];
     ks8 = f16x8{ks, ks, ks, ks, ks, ks, ks, ks};
 #pragma unroll
-    for (int x = 0; x < 2; ++x) kx[x] = expand8(lut, k_raw[x], lane4);
+    for (int x = 0; x < 2; ++x) kx[x] = expand8(lut, k_raw[x], 4u * (lane & 31));
     // values: 16 lanes fetch 16 positions of their 16 elements, in the order of the scores
     const int tr_pos = ((lane >> 3) & 1) * 16 + ((lane >> 2) & 1) * 8 + half * 4 + (lane & 3);
     vt = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
         (__attribute__((address_space(3))) i32x2*)(raw_v + (((lane >> 4) & 1) * 32 + tr_pos) * 8));
   };
   auto stage_keys = [&](int k) {
+    const int lane = my_lane(), half = lane >> 5;
     char* kbuf = smem + kPairBytes + (k & 1) * (2 * S::kOperand);
     const _Float16* vs_tab = reinterpret_cast<const _Float16*>(scales_of(k) + 256);
 #pragma unroll
     for (int x = 0; x < 2; ++x) *reinterpret_cast<f16x8*>(kbuf + ((wp * NS + 2 * wu + x) * 64 + lane) * 16) = kx[x] * ks8;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      vx[x] = expand8(lut, (uint32_t)vt[x], lane4);
+      vx[x] = expand8(lut, (uint32_t)vt[x], 4u * (lane & 31));
       const _Float16* vs = vs_tab + (wu >> 1) * kTile + 32 * wp + 16 * x + 4 * half;
       const u32x2 lo = *reinterpret_cast<const u32x2*>(vs), hi = *reinterpret_cast<const u32x2*>(vs + 8);
       vs8[x] = __builtin_bit_cast(f16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
     }
   };
   auto stage_values = [&](int k) {
+    const int lane = my_lane();
     char* vbuf = smem + kPairBytes + (k & 1) * (2 * S::kOperand) + S::kOperand;
 #pragma unroll
     for (int x = 0; x < 2; ++x) *reinterpret_cast<f16x8*>(vbuf + (((wu * NP + wp) * 2 + x) * 64 + lane) * 16) = vx[x] * vs8[x];
@@ -274,7 +285,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     scales_find(0);
   }
   char* turn = smem + wave * kTurn;
-  f16x8 q[NS];                                  // step s: elements 32 (s / 2) + 16 half + 8 (s % 2) ..
+  constexpr int kHeld = NS - S::kStored;
+  f16x8 q[kHeld];                               // step s: elements 32 (s / 2) + 16 half + 8 (s % 2) ..
+  char* q_stored = smem + S::kStoredOff + (wave * S::kStored * 64 + lane) * 16;
   float factor;
   {
     constexpr int kChunks = D / 8, kLoad = 64 / kChunks;   // chunks of a row, rows of a load
@@ -318,7 +331,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       u32x4 h;
 #pragma unroll
       for (int x = 0; x < 4; ++x) h[x] = pack_f16x2(bf16_lo(raw[s][x]) * down, bf16_hi(raw[s][x]) * down);
-      q[s] = __builtin_bit_cast(f16x8, h);
+      if (s < kHeld)
+        q[s] = __builtin_bit_cast(f16x8, h);
+      else
+        *reinterpret_cast<u32x4*>(q_stored + (s - kHeld) * 1024) = h;
     }
     factor = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * (kLog2e * lv.inv_kappa) * pow2(e2);
   }
@@ -365,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[p][i] = 0.f;
       // operands are read kAhead products before their use
-      constexpr int kAhead = 2;
+      constexpr int kAhead = D == 256 ? 3 : 2;
       f16x8 kf[kAhead];
       auto key = [&](int y) { return *reinterpret_cast<const f16x8*>(kbuf + ((y % NP * NS + y / NP) * 64 + lane) * 16); };
 #pragma unroll
@@ -374,12 +390,17 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int y = 0; y < NP * NS; ++y) {
         const f16x8 now_k = kf[y % kAhead];
         if (y + kAhead < NP * NS) kf[y % kAhead] = key(y + kAhead);
-        s[y % NP] = mfma32(now_k, q[y / NP], s[y % NP]);
+        const f16x8 now_q = y / NP < kHeld ? q[y / NP] : *reinterpret_cast<const f16x8*>(q_stored + (y / NP - kHeld) * 1024);
+        s[y % NP] = mfma32(now_k, now_q, s[y % NP]);
         if (D != 256 && y == 0) stage_fetch(k + 1);
         if (D != 256 && y == NP * NS * 3 / 4) stage_keys(k + 1);
       }
       if (D != 256) load_codes(k + 2);
       if (!(full && pos0 >= all_low && pos0 + kTile <= all_high)) {
+        int my_row = col;
+        asm volatile("" : "+v"(my_row));        // the row's ends are not worth registers during the loop
+        const int my_q = div_by(min(w0 + my_row, rows - 1), a.group_div);
+        const int qlow = seen_low(a, seq, my_q), qhigh = seen_high(a, seq, my_q);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           uint32_t ok = 0xFFFFFFFFu;
@@ -448,8 +469,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (y + kAhead < NU * NP * 2) vf[y % kAhead] = value(y + kAhead);
         o[y % NU] = mfma32(now_v, w[y / NU], o[y % NU]);
         if (D != 256 && y == NU * NP) stage_values(k + 1);
+        if (D == 256 && y == NU) stage_fetch(k + 1);
+        if (D == 256 && y == 2 * NU - 2) {
+          stage_keys(k + 1);
+          load_codes(k + 2);
+        }
       }
-      if (D == 256) stage_all(k);
+      if (D == 256) stage_values(k + 1);
     } else {
       stage_all(k);
     }
@@ -522,11 +548,11 @@ hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Pa
 }  // namespace
 
 // One workgroup fills a CU.  Measured with eight prompts of 16 .. 2000 tokens on 8 heads: 45,
-// 68 and 141 us at D = 64, 128, 256, the launch's 3 us among them, of which the longest
-// workgroup starts for 5 and takes 20, 31 and 67 ns a position (2.1 to 2.6 us a tile of
+// 68 and 129 us at D = 64, 128, 256, the launch's 3 us among them, of which the longest
+// workgroup starts for 5 and takes 20, 31 and 61 ns a position (2.0 to 2.6 us a tile of
 // 8192 / D).
 Cost prompt_cost(const AttnArgs& a) {
-  const float us = a.c.D == 64 ? 0.020f : a.c.D == 128 ? 0.031f : 0.067f;
+  const float us = a.c.D == 64 ? 0.020f : a.c.D == 128 ? 0.031f : 0.061f;
   return Cost{kRows, 1, 5.f, us};
 }
 
