@@ -226,10 +226,11 @@ static AttnPass best_pass(const AttnArgs& a) {
 // Prompts and single steps in one batch, which few tokens for seqs and max_q tell, take two
 // passes: one for the sequences of more than kStepRows query rows (and more than a query),
 // its tiles listed, as most of a grid of tiles and sequences would be empty, and one for
-// the others.  A prompt of 2048 and 63 steps on 4096 positions, 32 heads on 8 of 128: 591 us
-// in one pass, 237 us in two; a prompt of 8192 and 255 steps on 1000: 2618 and 774 us.
+// the others, a tile each (two tiles of 16 rows, mostly empty: 2 to 40 % more).  A prompt of
+// 2048 and 63 steps on 4096 positions, 32 heads on 8 of 128: 591 us in one pass, 213 us in
+// two; a prompt of 8192 and 255 steps on 1000: 2618 and 720 us.
 AttnPlan kv_attention_plan(const AttnArgs& a) {
-  constexpr int64_t kStepRows = 32;
+  constexpr int64_t kStepRows = 16;
   const int64_t group = a.q_heads / a.c.heads, step_q = std::max<int64_t>(1, kStepRows / group);
   auto workspace = [&](const Split& sp) {
     const int64_t tokens = sp.part_q ? a.seqs * sp.part_q : a.tokens;

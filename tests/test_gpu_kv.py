@@ -380,8 +380,8 @@ def test_prompts_with_their_positions_split(D, Hkv, n, window):
 @pytest.mark.parametrize("D,Hkv,G", [(64, 2, 4), (64, 24, 2), (128, 2, 1), (128, 1, 40), (128, 48, 1), (256, 2, 3)])
 @pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 50)])
 def test_prompts_and_steps_in_one_batch(D, Hkv, G, causal, window):
-    """Few tokens for the sequences and the longest one's queries: two passes, whose border is at 32 query rows."""
-    step = max(1, 32 // G)
+    """Few tokens for the sequences and the longest one's queries: two passes, whose border is at 16 query rows."""
+    step = max(1, 16 // G)
     queries = [130, 1, step, step + 1, 0, 2, 1] + [1] * 9 + [40]
     lengths = [max(n, x) for n, x in zip(queries, [333, 1, 77, 64, 5, 0, 100] + [17 * i for i in range(9)] + [200])]
     run_case(1480 + D + G, lengths, queries, Hkv, G, D, 16, 0, causal=causal, window=window, hide=(0, 3))
