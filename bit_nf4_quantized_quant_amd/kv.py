@@ -13,6 +13,14 @@ import functools
 
 from ._lib import _check, _i64, lib
 
+torch = None   # bound by the first cache: importing the package does not need it, and a statement a call costs 0.1 us
+_Strides2, _Strides4 = _i64 * 2, _i64 * 4
+
+
+def _bind_torch():
+    global torch
+    import torch
+
 
 class _CacheStruct(ctypes.Structure):
     """struct qlora_kv_cache"""
@@ -36,7 +44,7 @@ class KVCache:
     table: int = 0
 
     def __post_init__(self):
-        import torch
+        _bind_torch()
         pages, heads, page, half = self.k_codes.shape
         for name, dtype, last in (("k_codes", torch.uint8, half), ("v_codes", torch.uint8, half),
                                   ("k_scales", torch.bfloat16, half // 32), ("v_scales", torch.bfloat16, half // 32)):
@@ -69,7 +77,7 @@ class KVCache:
 
 def kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda", table: int = 0) -> KVCache:
     """An empty cache: every row reads back as zero."""
-    import torch
+    _bind_torch()
     if page_size < 1 or page_size % 16 or head_dim not in (64, 128, 256):
         raise ValueError("kv_cache: page_size must be a multiple of 16 and head_dim 64, 128 or 256")
     t = [torch.zeros((pages, kv_heads, page_size, n), dtype=d, device=device)
@@ -81,12 +89,10 @@ def _raw_stream(stream, device) -> int:
     """The hipStream_t of `stream`, or of the device's current stream.  (The raw
     query takes 0.1 us; building a torch.cuda.Stream for it takes 3 us, as long as
     the launch.)"""
-    import torch
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def _dtype_code(dtype) -> int:
-    import torch
     if dtype == torch.bfloat16:
         return 0
     if dtype == torch.float32:
@@ -96,7 +102,6 @@ def _dtype_code(dtype) -> int:
 
 def _ints(t, name, shape, device):
     """A contiguous int32 tensor on the cache's device, as a pointer."""
-    import torch
     if t.dtype != torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on the cache's device")
     return t.data_ptr()
@@ -115,14 +120,13 @@ def kv_write(k, v, cache: KVCache, slots, stream=None) -> None:
     if ks[2] != 1 or vs[2] != 1:
         raise ValueError("kv_write: the last axis of k and v must be contiguous")
     _check(lib().qlora_kv_write(cache._ref, k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype), n,
-                                (_i64 * 4)(ks[0], ks[1], vs[0], vs[1]), _ints(slots, "slots", (n,), device),
+                                _Strides4(ks[0], ks[1], vs[0], vs[1]), _ints(slots, "slots", (n,), device),
                                 _raw_stream(stream, device)), "qlora_kv_write")
 
 
 def kv_read(cache: KVCache, slots, dtype=None, stream=None):
     """The tokens at `slots` (int32 [n]) as (k, v), each [n, kv_heads, head_dim] in
     `dtype` (bf16 unless given; or fp32); zeros for a skipped slot."""
-    import torch
     if dtype is None:
         dtype = torch.bfloat16
     n, device = slots.shape[0], cache.k_codes.device
@@ -147,7 +151,6 @@ def kv_attention_workspace(cache: KVCache, q_heads: int, tokens: int, seqs: int,
                            window: int = 0):
     """A workspace for kv_attention calls of these sizes (any content), or None
     where they need none."""
-    import torch
     n = _workspace_bytes(cache.kv_heads, cache.page_size, cache.head_dim, q_heads, tokens, seqs, max_q, max_len, window)
     return torch.empty(n, dtype=torch.uint8, device=cache.k_codes.device) if n else None
 
@@ -167,7 +170,6 @@ def kv_attention(q, cache: KVCache, block_table, lengths, q_starts=None, max_q=N
     own (causal) or all, and only the last `window` of them where window > 0; one
     that sees none gets zeros and an lse of -infinity.
     """
-    import torch
     tokens, heads, dim = q.shape
     seqs, width = block_table.shape
     device = cache.k_codes.device
@@ -186,7 +188,7 @@ def kv_attention(q, cache: KVCache, block_table, lengths, q_starts=None, max_q=N
     if workspace is None:
         workspace = kv_attention_workspace(cache, heads, tokens, seqs, max_q, max_len, window)
     _check(lib().qlora_kv_attention(
-        cache._ref, q.data_ptr(), (_i64 * 2)(qs[0], qs[1]), tokens, heads,
+        cache._ref, q.data_ptr(), _Strides2(qs[0], qs[1]), tokens, heads,
         _ints(block_table, "block_table", (seqs, width), device), width, _ints(lengths, "lengths", (seqs,), device),
         None if q_starts is None else _ints(q_starts, "q_starts", (seqs + 1,), device), seqs, max_q, max_len,
         dim ** -0.5 if scale is None else scale, causal, window, out.data_ptr(),
