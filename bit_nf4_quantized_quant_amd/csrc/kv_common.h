@@ -74,13 +74,21 @@ __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
 __device__ __forceinline__ bool taken(const Split& sp, int rows) { return rows > sp.above && rows <= sp.upto; }
 
 // The sequence and the row tile of a pass's slot-th tile, by a wave: false if it has fewer.
+// A lane counts the tiles of four sequences at a time.
 __device__ __forceinline__ bool listed_tile(const AttnArgs& a, const Split& sp, int slot, int& b, int& tile) {
-  const int lane = threadIdx.x & 63, group = (int)a.group_div.d;
-  for (int b0 = 0; b0 < (int)a.seqs; b0 += 64) {
-    int q0 = 0, n = 0;
-    if (b0 + lane < (int)a.seqs) queries(a, b0 + lane, q0, n);
-    const int tiles = taken(sp, n * group) ? (n * group + sp.tile_rows - 1) / sp.tile_rows : 0;
-    int sum = tiles;
+  constexpr int kEach = 4;
+  const int lane = threadIdx.x & 63, group = (int)a.group_div.d, shift = __builtin_ctz(sp.tile_rows);
+  for (int b0 = 0; b0 < (int)a.seqs; b0 += 64 * kEach) {
+    int tiles[kEach], all = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int at = b0 + lane * kEach + e;
+      int q0 = 0, n = 0;
+      if (at < (int)a.seqs) queries(a, at, q0, n);
+      tiles[e] = taken(sp, n * group) ? (n * group + sp.tile_rows - 1) >> shift : 0;
+      all += tiles[e];
+    }
+    int sum = all;
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) {
       const int below = __shfl_up(sum, x);
@@ -89,8 +97,15 @@ __device__ __forceinline__ bool listed_tile(const AttnArgs& a, const Split& sp, 
     const uint64_t past = __ballot(sum > slot);
     if (past) {
       const int at = __builtin_ctzll(past);
-      b = b0 + at;
-      tile = slot - (__builtin_amdgcn_readlane(sum, at) - __builtin_amdgcn_readlane(tiles, at));
+      tile = slot - (__builtin_amdgcn_readlane(sum, at) - __builtin_amdgcn_readlane(all, at));
+      b = b0 + at * kEach;
+#pragma unroll
+      for (int e = 0; e < kEach - 1; ++e) {
+        const int these = __builtin_amdgcn_readlane(tiles[e], at);
+        if (tile < these) return true;
+        tile -= these;
+        ++b;
+      }
       return true;
     }
     slot -= __builtin_amdgcn_readlane(sum, 63);

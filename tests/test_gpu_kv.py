@@ -393,6 +393,13 @@ def test_prompts_and_steps_with_their_positions_split(D):
     run_case(1510 + D, [100] * 70 + [400, 900] + [30] * 5, [1] * 70 + [300, 200] + [3] * 5, 1, 4, D, 16, 0)
 
 
+@pytest.mark.parametrize("D,G,long", [(64, 1, 90), (128, 4, 300), (256, 2, 90)])
+def test_a_few_prompts_among_many_steps(D, G, long):
+    """Prompts far apart in a batch of more sequences than a wave looks at at once, the first and the last among them."""
+    queries = [40] + [1] * 253 + [long, 0, 37] + [1] * 300 + [31]
+    run_case(1520 + D, [n + 5 * (n > 1) + 3 for n in queries], queries, 1, G, D, 16, 0)
+
+
 def test_wide_heads_with_many_splits():
     run_case(1460, [6000, 2500], [1, 1], 2, 3, 256, 64, 0, uniform=True)
 
