@@ -5,7 +5,8 @@ projection and the o projection are QLoRA NF4 linears; keys and values go to a
 paged cache in NF4 codes as they are made, and attention reads them back from
 there.  A prompt of each sequence is taken in one call, then tokens one at a
 time; every step's output is compared with that of the whole sequence taken as
-one prompt, which sees the same codes.
+one prompt, which sees the same codes.  A sequence can also be forked: its tokens
+are read back and stored again in another one's pages, and both go on from there.
 
     python examples/decode_attention.py [--seqs 3] [--prompt 300] [--steps 8]
 """
@@ -57,6 +58,17 @@ class Block:
         return y.view(seqs, n, WIDTH)
 
 
+    def fork(self, source: int, target: int):
+        """Sequence `target` becomes a copy of `source`.  Storing what was read back gives the same values: the largest
+        magnitude of a run reads back as its scale."""
+        import torch
+        position = torch.arange(int(self.lengths[source]), device=self.lengths.device)
+        slots = self.pages[:, position // PAGE] * PAGE + (position % PAGE).int()
+        k, v = self.qa.kv_read(self.cache, slots[source].contiguous(), torch.float32)
+        self.qa.kv_write(k, v, self.cache, slots[target].contiguous())
+        self.lengths[target] = self.lengths[source]
+
+
 def run(seqs: int = 3, prompt: int = 300, steps: int = 8, seed: int = 0) -> float:
     """The largest relative difference (2-norm over a token's output) of the stepwise run from the one-prompt run."""
     import torch
@@ -69,6 +81,20 @@ def run(seqs: int = 3, prompt: int = 300, steps: int = 8, seed: int = 0) -> floa
     return float(((got - ref).norm(dim=-1) / ref.norm(dim=-1)).max())
 
 
+def run_forked(prompt: int = 300, steps: int = 4, seed: int = 0) -> float:
+    """The largest difference between a sequence's and its copy's outputs on the same further tokens."""
+    import torch
+    g = torch.Generator("cuda").manual_seed(seed)
+    block = Block(2, prompt + steps, g)
+    block.step(torch.randn((2, prompt, WIDTH), generator=g, device="cuda").bfloat16())
+    block.fork(0, 1)
+    off = 0.0
+    for _ in range(steps):
+        y = block.step(torch.randn((1, 1, WIDTH), generator=g, device="cuda").bfloat16().expand(2, 1, WIDTH)).float()
+        off = max(off, float((y[0] - y[1]).abs().max()))
+    return off
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--seqs", type=int, default=3)
@@ -77,6 +103,7 @@ def main():
     a = ap.parse_args()
     off = run(a.seqs, a.prompt, a.steps)
     print(f"{a.seqs} sequences, prompt of {a.prompt}, {a.steps} single tokens: largest difference from one prompt {off:.2e}")
+    print(f"a copy of a sequence after {a.prompt} tokens: largest difference {run_forked(a.prompt, a.steps):.2e}")
 
 
 if __name__ == "__main__":

@@ -500,6 +500,32 @@ def test_decoder_block_steps_match_one_prompt():
     assert example.run(seqs=2, prompt=150, steps=3) <= 2e-2
 
 
+def test_a_forked_sequence_goes_on_like_its_origin():
+    import os
+    import runpy
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_attention.py")
+    assert runpy.run_path(path)["run_forked"](prompt=131, steps=3) == 0.0
+
+
+@pytest.mark.parametrize("table", [0, 1, 2])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_storing_what_was_read_back_gives_the_same_values(D, table):
+    """The same scales, and the same codes but for FP4's, of whose two zeros the storing rule takes one."""
+    T, H = 97, 3
+    rng = np.random.default_rng(1600 + D + table)
+    x = (rng.normal(0, 1, (2, T, H, D)) * np.exp(rng.normal(0, 3, (2, T, H, 1)))).astype(np.float32)
+    first, second = (qa.kv_cache(-(-T // 16), 16, H, D, table=table) for _ in range(2))
+    slots = ints(rng.permutation(T))
+    qa.kv_write(dev_f32(x[0]), dev_f32(x[1]), first, slots)
+    k, v = qa.kv_read(first, slots, torch.float32)
+    qa.kv_write(k, v, second, slots)
+    for name, a, b in zip(("k_codes", "k_scales", "v_codes", "v_scales"), tensors(first), tensors(second)):
+        if table != 2 or name.endswith("scales"):
+            assert np.array_equal(a, b), name
+    for a, b in zip((k, v), qa.kv_read(second, slots, torch.float32)):
+        assert np.array_equal(host(a), host(b))
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_seeded_shapes(seed):
     rng = np.random.default_rng(9000 + seed)
