@@ -51,29 +51,36 @@ struct Seq {
   int64_t shift;   // query i stands at position shift + i
 };
 
-__device__ __forceinline__ void queries(const AttnArgs& a, int b, int& q0, int& n) {
-  if (a.q_starts) {
-    const int tokens = (int)a.tokens;
-    q0 = min(max(a.q_starts[b], 0), tokens);
-    n = min(min(max(a.q_starts[b + 1] - q0, 0), (int)a.max_q), tokens - q0);
-  } else {
-    q0 = b * (int)a.max_q;
-    n = (int)a.max_q;
-  }
+// What the batch says of a sequence: three loads under way at once (without q_starts two
+// of them fetch the length again, which nothing uses).
+struct Numbers {
+  int length, first, next;
+};
+__device__ __forceinline__ Numbers numbers(const AttnArgs& a, int b) {
+  const int32_t* starts = (a.q_starts ? a.q_starts : a.lengths) + b;
+  return Numbers{a.lengths[b], starts[0], starts[a.q_starts ? 1 : 0]};
 }
-__device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
+__device__ __forceinline__ void queries(const AttnArgs& a, int b, int first, int next, int& q0, int& n) {
+  const int tokens = (int)a.tokens, from = min(max(first, 0), tokens);
+  q0 = a.q_starts ? from : b * (int)a.max_q;
+  n = a.q_starts ? min(min(max(next - from, 0), (int)a.max_q), tokens - from) : (int)a.max_q;
+}
+__device__ __forceinline__ Seq sequence(const AttnArgs& a, int b, const Numbers& given) {
   Seq s;
-  const int length = a.lengths[b];
-  queries(a, b, s.q0, s.n);
+  const int length = given.length;
+  queries(a, b, given.first, given.next, s.q0, s.n);
   s.len = min(max(length, 0), (int)a.table_width * (int)a.c.page_size);
   s.shift = (int64_t)length - s.n;
   return s;
 }
 
+__device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) { return sequence(a, b, numbers(a, b)); }
+
 // Whether a pass is for a sequence of so many query rows.
 __device__ __forceinline__ bool taken(const Split& sp, int rows) { return rows > sp.above && rows <= sp.upto; }
 
-// The sequence and the row tile of a pass's slot-th tile, by a wave: false if it has fewer.
+// The sequence and the row tile of a pass's slot-th tile (of a batch with q_starts), by a
+// wave: false if it has fewer.
 // A lane counts the tiles of four sequences at a time.
 __device__ __forceinline__ bool listed_tile(const AttnArgs& a, const Split& sp, int slot, int& b, int& tile) {
   constexpr int kEach = 4;
@@ -84,7 +91,7 @@ __device__ __forceinline__ bool listed_tile(const AttnArgs& a, const Split& sp, 
     for (int e = 0; e < kEach; ++e) {
       const int at = b0 + lane * kEach + e;
       int q0 = 0, n = 0;
-      if (at < (int)a.seqs) queries(a, at, q0, n);
+      if (at < (int)a.seqs) queries(a, at, a.q_starts[at], a.q_starts[at + 1], q0, n);
       tiles[e] = taken(sp, n * group) ? (n * group + sp.tile_rows - 1) >> shift : 0;
       all += tiles[e];
     }

@@ -159,11 +159,12 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
   const int split = (blockIdx.x + (sp.listed ? slot : b)) % sp.splits;
   // the first pages are fetched, and the pair table is made, while the sequence's numbers
   // are on their way: without a window the positions start at 0
+  const Numbers given = numbers(a, b);
   const int32_t* table = a.block_table + (int64_t)b * a.table_width;
   const int t_lane = split * sp.chunk + ((lane >> 1) * kWaves + wave) * kTile + (lane & 1) * 16;
   const uint32_t early_page = a.table_width > 0 ? (uint32_t)table[min((int)div_by(t_lane, a.c.page_div), (int)a.table_width - 1)] : 0;
   build_pairs<kThreads>(lv, lut);
-  const Seq seq = sequence(a, b);
+  const Seq seq = sequence(a, b, given);
   const int rows = seq.n * group;
   if (r0 >= rows || !taken(sp, rows)) return;
   const int i_first = div_by(r0, a.group_div), i_last = div_by(min(r0 + kRows, rows) - 1, a.group_div);
@@ -449,6 +450,18 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
     const float f = exp2_fast(m[j] - (top == -INFINITY ? 0.f : top));
     // the row a thread sums: row me / 32, elements 2 (me % 32) of each run
     const int orow = me >> 5, r = r0 + 16 * j + orow;
+    const int i = div_by(r, a.group_div);
+    const int64_t out_row = (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
+    auto part_row = [&]() { return partial_row(a, sp, seq, b, i, head * group + (r - i * group)) * sp.splits + split; };
+    if (j > 0) __syncthreads();                 // (the rows before have been summed)
+#pragma unroll
+    for (int c = 0; c < 4 * NB; ++c) {
+      f32x4 v = o[j][c];
+      v *= f;
+      *reinterpret_cast<f32x4*>(buf + (wave * 16 + my_col) * P + 16 * c + 4 * my_quad) = v;
+    }
+    __syncthreads();
+    if (r >= rows) continue;                    // (whole waves, mostly: 32 threads take a row)
     float rtop = -INFINITY, rsum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) rtop = fmaxf(rtop, stats[(w * kNQ + j) * 16 + orow].x);
@@ -458,18 +471,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
       const float2 s = stats[(w * kNQ + j) * 16 + orow];
       rsum = __builtin_fmaf(exp2_fast(s.x - rref), s.y, rsum);
     }
-    const int i = div_by(r, a.group_div);
-    const int64_t out_row = (int64_t)(seq.q0 + i) * a.q_heads + head * group + (r - i * group);
-    auto part_row = [&]() { return partial_row(a, sp, seq, b, i, head * group + (r - i * group)) * sp.splits + split; };
     const float inv = rsum == 0.f ? 0.f : lv.inv_kappa / rsum;
-    if (j > 0) __syncthreads();                 // (the rows before have been summed)
-#pragma unroll
-    for (int c = 0; c < 4 * NB; ++c) {
-      f32x4 v = o[j][c];
-      v *= f;
-      *reinterpret_cast<f32x4*>(buf + (wave * 16 + my_col) * P + 16 * c + 4 * my_quad) = v;
-    }
-    __syncthreads();
 #pragma unroll
     for (int e = 0; e < NB; ++e) {
       float2 s = make_float2(0.f, 0.f);
@@ -478,14 +480,12 @@ __global__ void __launch_bounds__(kThreads, D == 64 || (D == 128 && kNQ == 1) ? 
         const float2 v = *reinterpret_cast<const float2*>(buf + (w * 16 + orow) * P + e * 64 + 2 * (me & 31));
         s.x += v.x, s.y += v.y;
       }
-      if (r < rows) {
-        if (live == 1)
-          reinterpret_cast<uint32_t*>(a.out + out_row * D + e * 64)[me & 31] = pack_bf16x2(s.x * inv, s.y * inv);
-        else
-          reinterpret_cast<float2*>(part.o + part_row() * D + e * 64)[me & 31] = s;
-      }
+      if (live == 1)
+        reinterpret_cast<uint32_t*>(a.out + out_row * D + e * 64)[me & 31] = pack_bf16x2(s.x * inv, s.y * inv);
+      else
+        reinterpret_cast<float2*>(part.o + part_row() * D + e * 64)[me & 31] = s;
     }
-    if (r < rows && (me & 31) == 0) {
+    if ((me & 31) == 0) {
       if (live > 1)
         part.stat[part_row()] = make_float2(rtop, rsum);
       else if (a.lse)
