@@ -167,7 +167,7 @@ hipError_t launch_join(const AttnArgs& a, const Split& sp, float inv_kappa, cons
 // and half the longest one's time if that is more; pieces of one length go in rounds.
 Split split_of(const AttnArgs& a, const Cost& cost, float* us) {
   constexpr int kMaxSplits = 128;
-  constexpr float kShared = 1.5f, kSharedBase = 1.3f;   // by which two workgroups on a CU slow each other
+  constexpr float kShared = 1.5f, kSharedBase = 1.6f;   // by which two workgroups on a CU slow each other
   constexpr float kJoin = 6.f;              // the joining launch, us: 4 on the device, and the host's 3.5
   constexpr float kJoinBytes = 6e6f;        // its bytes per us, written and read back
   const int64_t group = a.q_heads / a.c.heads, rows = a.max_q * group;

@@ -5,17 +5,17 @@
 //   out_i = sum_j softmax_j(scale q_i k_j) v_j
 //
 // What bounds it is the cache's bytes on long contexts, and a workgroup's own
-// way (about 6 us, and 1.4 us a round of its waves) on short ones.  Each cache
+// way (about 5 us, and 1.4 us a round of its waves) on short ones.  Each cache
 // row is read from HBM once and its codes are expanded in registers, by way of a
 // table of level pairs in LDS, straight into fp16 matrix operands.  The scales
 // never touch the operands: a key's scales multiply the scores of its 64-element
 // runs after the product, a value's multiply the softmax weights before it.
 //
-// Measured: two sequences of 131072 positions, 64 heads on 8 of 128: 63 us with
-// the joining, 285 MB at 4.5 TB/s (the kernel alone 58 us; in its middle it reads
+// Measured: two sequences of 131072 positions, 64 heads on 8 of 128: 62 us with
+// the joining, 285 MB at 4.6 TB/s (the kernel alone 58 us; in its middle it reads
 // 7 TB/s, the rest is the start and the joins); 32 sequences of 1 .. 4096
-// positions 30 us (2.5 TB/s: the longest sequences' workgroups walk twice the
-// mean); one sequence of 700, 32 heads 10.6 us.
+// positions 28.6 us (2.6 TB/s: the longest sequences' workgroups walk twice the
+// mean); one sequence of 700, 32 heads 9.8 us.
 //
 // Split.  A workgroup takes one kv head, 16 kNQ query rows and a chunk of the
 // positions; its eight waves take tiles of 32 positions in turn, each with its
@@ -504,16 +504,16 @@ hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Pa
 
 }  // namespace
 
-// Measured with eight sequences of 1000 positions: 6 us and, a position, 6.2 and 10.5 ns at
-// D = 64 and 128 with 32 rows, 5.0, 7.4 and 15.2 ns at D = 64, 128, 256 with 16.  So 40 rows on each of 32 pairs of
-// sequence and head, 1024 positions of 64, take 12.8 us in tiles of 32 and 9.8 us in tiles
-// of 16, but 64 rows on 128 pairs, 1000 positions of 128, 18.0 us and 20.2 us.  At D = 256
-// the registers hold 16 rows only (five queries of eight heads on 32 pairs, 4000 positions:
-// 101 us with 32, 47 us with 16).
+// Measured with batches that fill the device: 5 us and, a position, 6.2 and 10.5 ns at D =
+// 64 and 128 with 32 rows, 5.0, 7.4 and 15.2 ns at D = 64, 128, 256 with 16 (few workgroups
+// take two thirds of that).  So 40 rows on each of 32 pairs of sequence and head, 1024
+// positions of 64, take 11.2 us in tiles of 32 and 9.5 us in tiles of 16, but 64 rows on 128
+// pairs, 1000 positions of 128, 15.4 us and 19.1 us.  At D = 256 the registers hold 16 rows
+// only.
 Cost decode_cost(const AttnArgs& a, int rows) {
   const float ns = a.c.D == 256 ? 15.2f : a.c.D == 128 ? (rows == 16 ? 7.4f : 10.5f) : rows == 16 ? 5.0f : 6.2f;
   const int per_cu = a.c.D == 64 || (a.c.D == 128 && rows == 16) ? 2 : 1;
-  return Cost{rows, per_cu, 6.f, 1e-3f * ns};
+  return Cost{rows, per_cu, 5.f, 1e-3f * ns};
 }
 
 hipError_t launch_decode(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s) {

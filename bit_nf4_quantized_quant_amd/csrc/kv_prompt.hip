@@ -549,11 +549,11 @@ hipError_t launch(const AttnArgs& a, const Split& sp, const Levels& lv, const Pa
 
 // One workgroup fills a CU.  Measured with eight prompts of 16 .. 2000 tokens on 8 heads: 45,
 // 68 and 129 us at D = 64, 128, 256, the launch's 3 us among them, of which the longest
-// workgroup starts for 5 and takes 20, 31 and 61 ns a position (2.0 to 2.6 us a tile of
+// workgroup starts for 6 and takes 20, 31 and 61 ns a position (2.0 to 2.6 us a tile of
 // 8192 / D).
 Cost prompt_cost(const AttnArgs& a) {
   const float us = a.c.D == 64 ? 0.020f : a.c.D == 128 ? 0.031f : 0.061f;
-  return Cost{kRows, 1, 5.f, us};
+  return Cost{kRows, 1, 6.f, us};
 }
 
 hipError_t launch_prompt(const AttnArgs& a, const Split& sp, const Partial& part, hipStream_t s) {
